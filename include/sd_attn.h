@@ -452,6 +452,153 @@ SD_API sd_status sd_verify_attention_noalloc(const sd_q_desc *q, const void *q_d
                                       const sd_kv_desc *kv, int32_t batch, void *out,
                                       int32_t *dev_err, void *stream);
 
+/* ------------------------------------------------------------------ filling the cache ----
+ *
+ * Rotary position embedding of the rows of an append (NULL: no rotation).  Pair m of a head's
+ * first rotary_dim channels turns by angle = position * f_m:
+ *     (a, b) -> g (a cos - b sin, b cos + a sin)
+ * with the pairs (m, m + rotary_dim/2) in the half layout and (2m, 2m + 1) in the interleaved
+ * one; channels from rotary_dim on pass unchanged.  Frequencies, with r = rotary_dim:
+ *  SD_ROPE_UNSCALED  f_m = theta^(-2m/r)
+ *  SD_ROPE_LINEAR    f_m / factor (positions divided by factor)
+ *  SD_ROPE_NTK       (theta factor^(r/(r-2)))^(-2m/r); r >= 4
+ *  SD_ROPE_YARN      f_m (1 - t_m + t_m / factor), t_m = clamp((m - lo) / (hi - lo), 0, 1),
+ *                    lo = max(floor(c(32)), 0), hi = min(ceil(c(1)), r - 1) (lo + 0.001 if not
+ *                    above lo), c(n) = r ln(original_len / (2 pi n)) / (2 ln theta): pairs that
+ *                    turn more than 32 times within original_len keep their frequency, those
+ *                    that turn less than once are divided by factor
+ *  inv_freq          HOST array of r/2 floats, or NULL: the frequencies themselves (theta,
+ *                    scaling, factor and original_len are then not used)
+ *  gain              g, the factor of the cosine and the sine; 0 selects 1, or for
+ *                    SD_ROPE_YARN 0.1 ln(factor) + 1
+ * Angles are formed and reduced to one turn in 64 bits, so far positions lose nothing.
+ */
+typedef enum { SD_ROPE_HALF = 0, SD_ROPE_INTERLEAVED = 1 } sd_rope_layout;
+typedef enum {
+    SD_ROPE_UNSCALED = 0,
+    SD_ROPE_LINEAR = 1,
+    SD_ROPE_NTK = 2,
+    SD_ROPE_YARN = 3
+} sd_rope_scaling;
+
+typedef struct {
+    int32_t layout;       /* sd_rope_layout */
+    int32_t rotary_dim;   /* even, 2..head_dim */
+    int32_t scaling;      /* sd_rope_scaling */
+    float theta;          /* > 0; > 1 for SD_ROPE_YARN */
+    float factor;         /* >= 1 (scaled modes) */
+    int32_t original_len; /* >= 1 (SD_ROPE_YARN) */
+    const float *inv_freq;
+    float gain;           /* >= 0 */
+} sd_rope_desc;
+
+/*
+ * New rows of a batch of sequences, in the cache's dtype.  Row r's heads are dense:
+ * q[r*q_stride + h*head_dim + e] for h < h_q, k and v likewise for h < h_kv (strides in
+ * elements, at least heads * head_dim, so the three may be parts of one projection's output).
+ * Sequence b owns rows [q_start[b], q_start[b+1]) (device int32 [batch+1]); they are the LAST
+ * n of its cache's kv_len[b] positions, as in the attention calls: row i goes to position
+ * kv_len[b] - n + i.  Rows from q_start[batch] on (padding) are neither read nor written.
+ *
+ *  h_q         query heads (0 with q NULL: keys and values alone).
+ *  n_rows      host: rows that q, k and v hold; every q_start entry is at most n_rows.
+ *  max_kv_len  host hint >= every kv_len[b]: positions a contiguous cache has room for.
+ *  pos         device int32 [n_rows], or NULL: the rows' rotation positions (NULL: their
+ *              cache positions).
+ */
+typedef struct {
+    int32_t h_q;
+    int32_t n_rows;
+    int32_t max_kv_len;
+    const int32_t *q_start;
+    const int32_t *pos;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+} sd_rows_desc;
+
+/*
+ * Appends rows to a cache: rotates the queries and keys, writes the keys and values into the
+ * cache (contiguous or paged) and the rotated queries into q_out [n_rows][h_q][head_dim], ready
+ * for the attention calls.  head_dim 64 or 128; the rotation is computed in fp32 and rounded
+ * once.  q_out may be q itself when q_stride == h_q * head_dim; no other overlap is allowed.
+ * q_out must be given exactly when h_q > 0.  Neither the rows nor q_out need more alignment
+ * than their type's; 16-byte aligned pointers and strides take wide copies.
+ *
+ * A sequence with kv_len[b] < n, kv_len[b] > max_kv_len, more positions than max_pages_per_seq
+ * pages hold, or rows outside [0, n_rows] sets SD_DEVERR_SHAPE and is skipped; a page index
+ * outside the pool sets SD_DEVERR_PAGE and the row's key and value are skipped.  Two sequences
+ * must not own the slot of one new row.  n_rows == 0 returns SD_OK and launches nothing.
+ */
+SD_API sd_status sd_kv_append(const sd_rope_desc *rope, const sd_rows_desc *rows,
+                              const sd_kv_desc *cache, int32_t batch, void *q_out,
+                              int32_t *dev_err, void *stream);
+
+/*
+ * KV cache held in 4 bits.  A row x of head_dim channels (one position of one KV head, of K
+ * or of V) is kept as codes c and two bf16 parameters, a scale s and a low value lo:
+ *     lo = bf16(min x), s = bf16((max x - lo) / 15) (0 if max x <= lo),
+ *     c_e = clamp(round((x_e - lo) / s), 0, 15), ties to even (0 if s == 0)
+ * and stands for lo + s c_e: (head_dim/2 + 4) bytes instead of 2 head_dim.  A row that holds an
+ * infinity or a NaN, or whose max x - lo overflows fp32, is kept as s = 0, lo = NaN (so it stands
+ * for NaN, which the attention of the rows that see it returns) and sets SD_DEVERR_NUMERIC.
+ *
+ *  dtype        type of the appended rows, and of Q and O of the attention: SD_F32 or SD_BF16.
+ *  head_dim     64 or 128.
+ *  k, v         codes, head_dim/2 bytes a row: channel 2i in the low half of byte i, channel
+ *               2i + 1 in its high half.  16-byte aligned.
+ *  k_param, v_param  4 bytes a row: bf16 s, then bf16 lo.  4-byte aligned.
+ *  Row numbers: contiguous (page_size == 0) b*stride_b + h*stride_h + j (strides in rows);
+ *               paged (page_size == 16) (page*h_kv + h)*16 + j%16 with
+ *               page = block_table[b*max_pages_per_seq + j/16].
+ *  kv_len       device int32 [batch].
+ */
+typedef struct {
+    int32_t dtype;
+    int32_t h_kv;
+    int32_t head_dim;
+    int32_t page_size;
+    void *k, *v;
+    void *k_param, *v_param;
+    int64_t stride_b, stride_h;
+    const int32_t *block_table;
+    int32_t max_pages_per_seq;
+    int32_t num_pages;
+    const int32_t *kv_len;
+} sd_kv4_desc;
+
+/*
+ * sd_kv_append into a 4-bit cache.  A key is rotated in 64 bits and rounded to the rows' type
+ * before it is quantised, so its codes do not depend on how a rotation rounds.  k_out and
+ * v_out ([n_rows][h_kv][head_dim] in the rows' type, each may be NULL) receive the values that
+ * the stored rows stand for: what attention over the cache will see, for a prompt's own
+ * attention.  q_out as in sd_kv_append, and so are errors and skipped rows.
+ */
+SD_API sd_status sd_kv4_append(const sd_rope_desc *rope, const sd_rows_desc *rows,
+                               const sd_kv4_desc *cache, int32_t batch, void *q_out, void *k_out,
+                               void *v_out, int32_t *dev_err, void *stream);
+
+/*
+ * Workspace bytes of sd_kv4_verify_attention with these descriptors (host values only).
+ */
+SD_API sd_status sd_kv4_attention_workspace_size(const sd_q_desc *q, const sd_kv4_desc *kv,
+                                                 int32_t batch, size_t *bytes);
+
+/*
+ * Dense attention over a 4-bit cache: what sd_verify_attention computes, with the values that
+ * the cache's rows stand for as K and V.  One row per sequence is plain decoding.  q_data and
+ * out hold kv->dtype.  Neither K nor V is ever dequantised in memory: scores are formed on the
+ * codes themselves (exact in bf16) and corrected by each row's s and lo, and V's scale is folded
+ * into the softmax weights.  bf16 rows run on tensor cores (up to 128 rows per KV head, q_data
+ * and out 16-byte aligned), the rest on CUDA cores.  workspace: 16-byte aligned, not shared
+ * with a call in flight.  A sequence whose hints are violated (more than max_q_rows rows, kv_len
+ * below its rows or above max_kv_len or its pages) sets SD_DEVERR_SHAPE and its rows of out are
+ * left as they were; rows on a page outside the pool (SD_DEVERR_PAGE) count as zeros.
+ */
+SD_API sd_status sd_kv4_verify_attention(const sd_q_desc *q, const void *q_data,
+                                         const sd_kv4_desc *kv, int32_t batch, void *out,
+                                         void *workspace, size_t workspace_bytes,
+                                         int32_t *dev_err, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -184,4 +184,69 @@ sd_status verify_run(const sd_q_desc *q, const void *q_data, const sd_kv_desc *k
                      void *out, const AttnPlan &plan, void *workspace, int32_t *dev_err,
                      void *stream);
 
+// Appending rows to a cache (dense or 4-bit).
+struct RopeParams {
+    int layout;
+    int rotary_dim;    // 0: no rotation
+    double gain;       // factor of the cosine and the sine
+    double turns[64];  // frequency of pair m in turns per position
+};
+
+struct AppendParams {
+    int dtype;     // of the rows, q_out, k_out and v_out
+    int kv4;       // 4-bit cache
+    int head_dim;
+    int h_q, h_kv;
+    int batch;
+    int n_rows, rows_per_block;
+    int max_kv_len;
+    const int32_t *q_start, *pos, *kv_len;
+    const void *q, *k, *v;  // rows; strides in elements
+    int64_t q_stride, k_stride, v_stride;
+    void *q_out, *k_out, *v_out;
+    // the cache: strides in elements (dense) or rows (4-bit)
+    int page_size;
+    void *k_cache, *v_cache;
+    uint32_t *k_param, *v_param;
+    int64_t stride_b, stride_h;
+    const int32_t *block_table;
+    int max_pages, num_pages;
+    RopeParams rope;
+    int32_t *dev_err;
+};
+// wide: every pointer and stride allows 16-byte accesses.
+cudaError_t launch_append(AppendParams p, bool wide, cudaStream_t s);
+
+// Attention over a 4-bit cache.
+struct Kv4Params {
+    const unsigned char *k, *v;     // codes
+    const uint32_t *kp, *vp;        // (scale, low) pairs
+    int page_size;
+    int64_t stride_b, stride_h;     // rows
+    const int32_t *block_table;
+    int max_pages, num_pages;
+    const int32_t *kv_len;
+    int dtype;
+    int head_dim;
+    int h_kv;
+    int batch;
+    int h_q;
+    int group;       // h_q / h_kv
+    int max_q_rows;  // host hints
+    int max_kv_len;
+    int rows_cap;    // batch * max_q_rows
+    float scale_log2;
+    const void *q;
+    const int32_t *q_start;
+    void *out;
+    int n_splits;    // CUDA-core engine: splits of every sequence's positions
+    int ctas;        // tensor-core engines: CTAs that share all units' tiles (0: CUDA cores)
+    int n_slots;     // partial results that ws holds, [n_slots][group * max_q_rows] rows each
+    float *ws;
+    int32_t *dev_err;
+};
+int kv4_simt_splits(int batch, int h_kv, int rows, int max_kv_len);
+cudaError_t launch_kv4_simt(const Kv4Params &p, cudaStream_t s);
+cudaError_t launch_kv4_merge(const Kv4Params &p, cudaStream_t s);
+
 }  // namespace sd

@@ -25,6 +25,8 @@ SD_ENGINE_CUDA_CORE, SD_ENGINE_TC, SD_ENGINE_TC_PERSISTENT = 0, 1, 2
 SD_TOPK_LAST_QUERY, SD_TOPK_MEAN_TEXT_ATTENTION = 0, 1
 SD_DEVERR_PAGE, SD_DEVERR_INDEX, SD_DEVERR_TOKEN, SD_DEVERR_NUMERIC, SD_DEVERR_SHAPE = 1, 2, 4, 8, 16
 SD_DEVERR_TIMEOUT = 32
+SD_ROPE_HALF, SD_ROPE_INTERLEAVED = 0, 1
+SD_ROPE_UNSCALED, SD_ROPE_LINEAR, SD_ROPE_NTK, SD_ROPE_YARN = 0, 1, 2, 3
 PAGE_SIZE = 16
 
 _LIB = None
@@ -58,7 +60,9 @@ EXPORTS = ("sd_status_string", "sd_version", "sd_attention_workspace_size", "sd_
            "sd_accept_sample", "sd_verify_attention_noalloc", "sd_sparse_workspace_size",
            "sd_sparse_selection_size", "sd_sparse_stage", "sd_sparse_attention_staged",
            "sd_topk_scored_workspace_size", "sd_topk_select_scored", "sd_set_wait_timeout_ns",
-           "sd_draft_layer_workspace_size", "sd_draft_layer", "sd_attention_plan")
+           "sd_draft_layer_workspace_size", "sd_draft_layer", "sd_attention_plan",
+           "sd_kv_append", "sd_kv4_append", "sd_kv4_attention_workspace_size",
+           "sd_kv4_verify_attention")
 
 # Size of the library's fixed scratch used by sd_verify_attention_noalloc.
 SD_VERIFY_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -105,6 +109,10 @@ def lib():
                                                             ctypes.POINTER(SZ)]
                 h.sd_topk_select_scored.argtypes = [ctypes.c_int, P, P, P, I32, P, P, I32, I32, P,
                                                     P, P, SZ, P, P]
+                h.sd_kv_append.argtypes = [P, P, P, I32, P, P, P]
+                h.sd_kv4_append.argtypes = [P, P, P, I32, P, P, P, P, P]
+                h.sd_kv4_attention_workspace_size.argtypes = [P, P, I32, ctypes.POINTER(SZ)]
+                h.sd_kv4_verify_attention.argtypes = [P, P, P, I32, P, P, SZ, P, P]
                 for name in EXPORTS[2:]:
                     if name not in ("sd_set_wait_timeout_ns",):
                         getattr(h, name).restype = ctypes.c_int
@@ -496,3 +504,242 @@ def sd_accept_sample(tgt_logits, draft_logits, draft_tok, u, v, gamma, max_gamma
                                       _ptr(near_boundary), _ptr(ws), ws.numel(), _ptr(dev_err),
                                       _stream(stream)), "sd_accept_sample")
     return n_acc, out_tok, near_boundary
+
+
+class sd_rope_desc(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("theta", ctypes.c_float),
+                ("factor", ctypes.c_float), ("original_len", ctypes.c_int32),
+                ("inv_freq", ctypes.c_void_p), ("gain", ctypes.c_float)]
+
+
+class sd_rows_desc(ctypes.Structure):
+    _fields_ = [("h_q", ctypes.c_int32), ("n_rows", ctypes.c_int32),
+                ("max_kv_len", ctypes.c_int32), ("q_start", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
+class sd_kv4_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_param", ctypes.c_void_p), ("v_param", ctypes.c_void_p),
+                ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("block_table", ctypes.c_void_p), ("max_pages_per_seq", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("kv_len", ctypes.c_void_p)]
+
+
+class Rope:
+    """The rotation of an append (see sd_rope_desc): ``rotary_dim`` channels of every query and
+    key head, in the half or interleaved layout, optionally scaled for a longer context.
+    ``inv_freq``: the frequencies themselves (rotary_dim/2 numbers, kept in fp32 on the host),
+    instead of theta and the scaling."""
+
+    def __init__(self, rotary_dim: int, theta: float = 10000.0, layout: int = SD_ROPE_HALF,
+                 scaling: int = SD_ROPE_UNSCALED, factor: float = 1.0, original_len: int = 0,
+                 inv_freq=None, gain: float = 0.0):
+        d = sd_rope_desc()
+        d.layout, d.rotary_dim, d.scaling = int(layout), int(rotary_dim), int(scaling)
+        d.theta, d.factor, d.gain = float(theta), float(factor), float(gain)
+        d.original_len = int(original_len)
+        if inv_freq is not None:
+            table = [float(f) for f in inv_freq]
+            if 2 * len(table) != d.rotary_dim:
+                raise ValueError("Rope: inv_freq holds rotary_dim / 2 frequencies")
+            self._table = (ctypes.c_float * len(table))(*table)
+            d.inv_freq = ctypes.cast(self._table, ctypes.c_void_p)
+        self.desc = d
+
+
+def _row_tensor(t: torch.Tensor, rows: int, what: str) -> int:
+    """Row stride of [rows][heads][head_dim] with dense rows (others raise)."""
+    if not t.is_cuda:
+        raise ValueError("sdattn: tensors must live on the GPU")
+    if t.dim() != 3 or t.shape[0] != rows or t.stride(2) != 1 or \
+            (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"NewRows: {what} must be [rows][heads][head_dim] with dense rows")
+    # (a single row's stride may be anything)
+    return t.stride(0) if rows > 1 else t.shape[1] * t.shape[2]
+
+
+class NewRows:
+    """Rows to append: ``k``, ``v`` [rows][h_kv][head_dim] and optionally ``q`` [rows][h_q][head_dim]
+    (each row dense; the three may be slices of one projection's output), ``q_start`` [batch+1]
+    (int32, GPU; the rows of sequence b are the last of its cache) and the hint ``max_kv_len``.
+    ``pos``: int32 [rows], the rows' rotation positions (default: their cache positions)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, max_kv_len: int,
+                 q: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None):
+        n = k.shape[0]
+        if v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("NewRows: k and v must have one shape and dtype")
+        if q is not None and (q.dtype != k.dtype or q.shape[-1] != k.shape[-1]):
+            raise ValueError("NewRows: q must have the dtype and head_dim of k")
+        for name, t, size in (("q_start", q_start, None), ("pos", pos, n)):
+            if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or
+                                  (size is not None and t.shape[0] != size)):
+                raise ValueError(f"NewRows: {name} must be an int32 vector of the right length")
+        for t in (v, q, q_start, pos):
+            if t is not None and t.device != k.device:
+                raise ValueError("NewRows: tensors must live on one device")
+        self.q, self.k, self.v, self.q_start, self.pos = q, k, v, q_start, pos
+        self.dtype = _dtype_code(k)
+        self.batch = q_start.shape[0] - 1
+        d = sd_rows_desc()
+        d.n_rows, d.max_kv_len = n, int(max_kv_len)
+        d.k, d.v = k.data_ptr(), v.data_ptr()
+        d.k_stride, d.v_stride = _row_tensor(k, n, "k"), _row_tensor(v, n, "v")
+        d.q_start, d.pos = _ptr(q_start), _ptr(pos)
+        if q is not None:
+            d.h_q, d.q, d.q_stride = q.shape[1], q.data_ptr(), _row_tensor(q, n, "q")
+        self.desc = d
+
+
+class KV4Cache:
+    """A cache held in 4 bits plus its C descriptor (see sd_kv4_desc).
+
+    Contiguous: codes ``k``, ``v`` uint8 [batch][h_kv][l_cap][head_dim/2] and parameters
+    ``k_param``, ``v_param`` bfloat16 [batch][h_kv][l_cap][2] (scale, low).  Paged: the same with
+    [num_pages][h_kv][16] in place of [batch][h_kv][l_cap], and ``block_table`` [batch][max_pages]
+    int32.  ``kv_len``: int32 [batch].  ``dtype``: type of the rows appended and of the attention's
+    queries and output."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_param: torch.Tensor,
+                 v_param: torch.Tensor, kv_len: torch.Tensor,
+                 block_table: Optional[torch.Tensor] = None, dtype=torch.bfloat16):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != torch.uint8 or v.dtype != torch.uint8:
+            raise ValueError("KV4Cache: k and v must be 4-D uint8 tensors of one shape")
+        if k_param.shape != k.shape[:3] + (2,) or v_param.shape != k_param.shape or \
+                k_param.dtype != torch.bfloat16 or v_param.dtype != torch.bfloat16:
+            raise ValueError("KV4Cache: k_param and v_param must be bfloat16 [...][2] beside k")
+        for t in (kv_len, block_table):
+            if t is not None and t.dtype != torch.int32:
+                raise ValueError("KV4Cache: kv_len and block_table must be int32")
+        for t in (v, k_param, v_param, kv_len, block_table):
+            if t is not None and t.device != k.device:
+                raise ValueError("KV4Cache: tensors must live on one device")
+        self.k, self.v, self.k_param, self.v_param = k, v, k_param, v_param
+        self.kv_len, self.block_table, self.dtype = kv_len, block_table, dtype
+        d = sd_kv4_desc()
+        d.dtype = {torch.bfloat16: SD_BF16, torch.float32: SD_F32}.get(dtype, -1)
+        if d.dtype < 0:
+            raise ValueError(f"sdattn: unsupported dtype {dtype}")
+        d.h_kv, d.head_dim = k.shape[1], 2 * k.shape[3]
+        d.k, d.v, d.k_param, d.v_param = _ptr(k), _ptr(v), _ptr(k_param), _ptr(v_param)
+        if block_table is None:
+            d.page_size = 0
+            d.stride_b, d.stride_h = k.shape[1] * k.shape[2], k.shape[2]
+            if kv_len.shape[0] != k.shape[0]:
+                raise ValueError("KV4Cache: kv_len must hold one length per sequence")
+        else:
+            if k.shape[2] != PAGE_SIZE:
+                raise ValueError("KV4Cache: paged caches use pages of 16 positions")
+            if block_table.dim() != 2 or block_table.shape[0] != kv_len.shape[0]:
+                raise ValueError("KV4Cache: block_table must hold one row per sequence")
+            d.page_size = PAGE_SIZE
+            d.block_table = _ptr(block_table)
+            d.max_pages_per_seq = block_table.shape[1]
+            d.num_pages = k.shape[0]
+        d.kv_len = _ptr(kv_len)
+        self.desc = d
+
+    @classmethod
+    def empty(cls, batch: int, h_kv: int, l_cap: int, head_dim: int, kv_len: torch.Tensor,
+              dtype=torch.bfloat16) -> "KV4Cache":
+        """A contiguous cache with room for l_cap positions per sequence, on kv_len's device."""
+        new = lambda w, t: torch.empty((batch, h_kv, l_cap, w), dtype=t, device=kv_len.device)  # noqa: E731
+        c = lambda: new(head_dim // 2, torch.uint8)  # noqa: E731
+        p = lambda: new(2, torch.bfloat16)  # noqa: E731
+        return cls(c(), c(), p(), p(), kv_len, dtype=dtype)
+
+    @property
+    def batch(self) -> int:
+        return self.kv_len.shape[0]
+
+    @property
+    def h_kv(self) -> int:
+        return self.k.shape[1]
+
+    @property
+    def head_dim(self) -> int:
+        return 2 * self.k.shape[3]
+
+
+def _check_rows(rows: NewRows, cache, where: str):
+    d, c = rows.desc, cache.desc
+    if rows.dtype != c.dtype or rows.k.shape[1] != c.h_kv or rows.k.shape[2] != c.head_dim:
+        raise ValueError(f"{where}: the rows' dtype, KV heads and head_dim must be the cache's")
+    if rows.batch != cache.batch or rows.k.device != cache.k.device:
+        raise ValueError(f"{where}: rows and cache must hold one batch on one device")
+    if c.page_size == 0 and d.max_kv_len > cache.k.shape[2]:
+        raise ValueError(f"{where}: max_kv_len exceeds the cache's room")
+
+
+def _rows_out(out, like: Optional[torch.Tensor], where: str):
+    """The caller's output for rows shaped as `like`, or a new one."""
+    if like is None:
+        if out is not None:
+            raise ValueError(f"{where}: q_out without q")
+        return None
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device:
+        raise ValueError(f"{where}: an output must have the shape, dtype and device of its rows")
+    return out
+
+
+def sd_kv_append(rope: Optional[Rope], rows: NewRows, cache: KVCache, q_out=None, dev_err=None,
+                 stream=None) -> Optional[torch.Tensor]:
+    """Rotates the rows' queries and keys and writes keys and values into the cache, whose kv_len
+    already counts them.  Returns the rotated queries (None without queries)."""
+    _check_rows(rows, cache, "sd_kv_append")
+    q_out = _rows_out(q_out, rows.q, "sd_kv_append")
+    with _on(rows.k):
+        _check(lib().sd_kv_append(ctypes.byref(rope.desc) if rope is not None else None,
+                                  ctypes.byref(rows.desc), ctypes.byref(cache.desc), cache.batch,
+                                  _ptr(q_out), _ptr(dev_err), _stream(stream)), "sd_kv_append")
+    return q_out
+
+
+def sd_kv4_append(rope: Optional[Rope], rows: NewRows, cache: KV4Cache, q_out=None, k_out=None,
+                  v_out=None, dev_err=None, stream=None) -> Optional[torch.Tensor]:
+    """sd_kv_append into a 4-bit cache.  k_out, v_out: optional tensors like the rows' k and v that
+    receive the values the stored rows stand for."""
+    _check_rows(rows, cache, "sd_kv4_append")
+    q_out = _rows_out(q_out, rows.q, "sd_kv4_append")
+    for t in (k_out, v_out):
+        if t is not None:
+            _rows_out(t, rows.k, "sd_kv4_append")
+    with _on(rows.k):
+        _check(lib().sd_kv4_append(ctypes.byref(rope.desc) if rope is not None else None,
+                                   ctypes.byref(rows.desc), ctypes.byref(cache.desc), cache.batch,
+                                   _ptr(q_out), _ptr(k_out), _ptr(v_out), _ptr(dev_err),
+                                   _stream(stream)), "sd_kv4_append")
+    return q_out
+
+
+def sd_kv4_attention_workspace_size(q: Queries, kv: KV4Cache) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().sd_kv4_attention_workspace_size(ctypes.byref(q.desc), ctypes.byref(kv.desc),
+                                                 kv.batch, ctypes.byref(n)),
+           "sd_kv4_attention_workspace_size")
+    return n.value
+
+
+def sd_kv4_verify_attention(q: Queries, kv: KV4Cache, out=None, workspace=None, dev_err=None,
+                            stream=None) -> torch.Tensor:
+    """Dense attention of the queries over a 4-bit cache (sd_verify_attention's mask)."""
+    if q.q.dtype != kv.dtype or q.q.shape[2] != kv.head_dim or q.q_start.shape[0] != kv.batch + 1:
+        raise ValueError("sd_kv4_verify_attention: queries and cache differ in dtype, head_dim or "
+                         "batch")
+    if kv.block_table is None and q.desc.max_kv_len > kv.k.shape[2]:
+        raise ValueError("sd_kv4_verify_attention: max_kv_len exceeds the cache's room")
+    out = _rows_out(out, q.q, "sd_kv4_verify_attention")
+    ws = _workspace(lambda: sd_kv4_attention_workspace_size(q, kv), q.q.device, workspace)
+    with _on(q.q):
+        _check(lib().sd_kv4_verify_attention(ctypes.byref(q.desc), _ptr(q.q),
+                                             ctypes.byref(kv.desc), kv.batch, _ptr(out), _ptr(ws),
+                                             ws.numel(), _ptr(dev_err), _stream(stream)),
+               "sd_kv4_verify_attention")
+    return out

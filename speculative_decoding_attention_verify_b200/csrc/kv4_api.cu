@@ -127,7 +127,8 @@ sd_status fill_rows(const sd_rope_desc *rope, const sd_rows_desc *rows, int dtyp
 sd_status status_of(cudaError_t e) { return e == cudaSuccess ? SD_OK : SD_ERR_CUDA; }
 
 struct Kv4Plan {
-    int n_splits, ctas, n_slots;
+    int n_splits, simt_slots;  // CUDA-core engine
+    int ctas;                  // tensor-core engine (0: not for this call)
     size_t ws_bytes;
 };
 
@@ -145,8 +146,12 @@ sd_status plan_kv4(const sd_q_desc *q, const sd_kv4_desc *kv, int batch, Kv4Plan
         return SD_ERR_INVALID_ARG;
     *plan = Kv4Plan{};
     plan->n_splits = kv4_simt_splits(batch, kv->h_kv, (int)rows, q->max_kv_len);
-    plan->n_slots = plan->n_splits > 1 ? batch * kv->h_kv * plan->n_splits : 0;
-    plan->ws_bytes = (size_t)plan->n_slots * rows * (kv->head_dim + 2) * sizeof(float);
+    plan->simt_slots = plan->n_splits > 1 ? batch * kv->h_kv * plan->n_splits : 0;
+    if (kv->dtype == SD_BF16 && rows <= kv4_mma_max_rows())
+        plan->ctas = kv4_mma_ctas(batch, kv->h_kv, q->max_kv_len);
+    // (whichever engine the pointers' alignment leaves)
+    const int slots = plan->simt_slots > 2 * plan->ctas ? plan->simt_slots : 2 * plan->ctas;
+    plan->ws_bytes = (size_t)slots * rows * (kv->head_dim + 2) * sizeof(float);
     return SD_OK;
 }
 
@@ -268,12 +273,17 @@ sd_status sd_kv4_verify_attention(const sd_q_desc *q, const void *q_data, const 
     p.q = q_data;
     p.q_start = q->q_start;
     p.out = out;
-    p.n_splits = plan.n_splits;
-    p.ctas = plan.ctas;
-    p.n_slots = plan.n_slots;
     p.ws = static_cast<float *>(workspace);
     p.dev_err = dev_err;
-    return status_of(launch_kv4_simt(p, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (plan.ctas && aligned(q_data, 16) && aligned(out, 16)) {
+        p.ctas = plan.ctas;
+        p.n_slots = 2 * plan.ctas;
+        return status_of(launch_kv4_mma(p, s));
+    }
+    p.n_splits = plan.n_splits;
+    p.n_slots = plan.simt_slots;
+    return status_of(launch_kv4_simt(p, s));
 }
 
 }  // extern "C"

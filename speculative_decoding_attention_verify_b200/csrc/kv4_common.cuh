@@ -83,6 +83,11 @@ __device__ __forceinline__ void kv4_count(const Kv4Params &p, int b, long long *
     }
 }
 
+// CTAs that take part: no more than there are tiles, so that each has one at least.
+__device__ __forceinline__ int kv4_ctas(const Kv4Params &p, long long total) {
+    return (int)(total < p.ctas ? total : p.ctas);
+}
+
 // CTA of G that holds tile x of T.
 __device__ __forceinline__ int kv4_cta_of(long long x, long long total, int ctas) {
     return (int)(((x + 1) * ctas - 1) / total);
@@ -95,6 +100,99 @@ __device__ __forceinline__ float *kv4_slot_o(const Kv4Params &p, int64_t slot, i
 __device__ __forceinline__ float *kv4_slot_ml(const Kv4Params &p, int64_t slot, int lr) {
     const int64_t rows = p.group * p.max_q_rows;
     return p.ws + (int64_t)p.n_slots * rows * p.head_dim + (slot * rows + lr) * 2;
+}
+
+// A position in the list of tiles: tile t of unit (b, g), with the sequence's row data.
+struct Kv4Cursor {
+    int b, g, t, tiles;
+    int q0, n_q, kv_len;
+    // Sequence b or the next one with work (b = batch at the end).
+    __device__ __forceinline__ void load(const Kv4Params &p) {
+        for (; b < p.batch; ++b) {
+            bool bad;
+            if (kv4_sequence(p, b, q0, n_q, kv_len, bad)) {
+                tiles = (kv_len + kKv4Tile - 1) / kKv4Tile;
+                return;
+            }
+        }
+        tiles = 1;
+        kv_len = 0;
+    }
+    // n tiles on, within the unit or to the start of the next one.
+    __device__ __forceinline__ void skip(const Kv4Params &p, int n) {
+        t += n;
+        if (t < tiles) return;
+        t = 0;
+        if (++g < p.h_kv) return;
+        g = 0;
+        ++b;
+        load(p);
+    }
+    __device__ __forceinline__ void next(const Kv4Params &p) { skip(p, 1); }
+};
+
+struct Kv4Start {
+    int b;
+    long long before;  // tiles of one KV head before sequence b
+};
+
+// The CTA's range [lo, hi) of the list of tiles, and the cursor at lo.  Every thread of the block
+// calls it; s_red holds 2 * NT / 32 values.  CTA 0 reports violated hints.
+template <int NT>
+__device__ __forceinline__ Kv4Cursor kv4_first(const Kv4Params &p, long long *s_red,
+                                               Kv4Start *s_start, long long &lo, long long &hi) {
+    constexpr int W = NT / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    long long total = 0, unused;
+    kv4_count<NT>(p, 0, s_red, total, unused);
+    if (blockIdx.x == 0)
+        for (int i = tid; i < p.batch; i += NT) {
+            int q0, n_q, kv_len;
+            bool bad;
+            if (!kv4_sequence(p, i, q0, n_q, kv_len, bad) && bad)
+                set_dev_err(p.dev_err, SD_DEVERR_SHAPE);
+        }
+    const long long all = total * p.h_kv;
+    const int ctas = kv4_ctas(p, all);
+    Kv4Cursor c{};
+    lo = hi = 0;
+    if ((int)blockIdx.x >= ctas) return c;
+    lo = all * blockIdx.x / ctas;
+    hi = all * (blockIdx.x + 1) / ctas;
+    // the sequence that holds tile lo: prefix sums over NT sequences at a time
+    const long long want = lo / p.h_kv;  // (before b) <= want < (before b + 1)
+    long long base = 0;
+    for (int i0 = 0; i0 < p.batch && base <= want; i0 += NT) {
+        const int i = i0 + tid;
+        const int n = i < p.batch ? kv4_tiles(p, i) : 0;
+        long long x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();  // (the last use of s_red)
+        if (lane == 31) s_red[warp] = x;
+        __syncthreads();
+        long long chunk = 0, mine = base + x - n;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) mine += s_red[w];
+            chunk += s_red[w];
+        }
+        if (n > 0 && mine <= want && want < mine + n) {
+            s_start->b = i;
+            s_start->before = mine;
+        }
+        base += chunk;
+    }
+    __syncthreads();
+    c.b = s_start->b;
+    c.load(p);
+    const long long in = lo - s_start->before * p.h_kv;
+    c.g = (int)(in / c.tiles);
+    c.t = (int)(in % c.tiles);
+    return c;
 }
 
 }  // namespace sd

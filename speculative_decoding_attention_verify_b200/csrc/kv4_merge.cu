@@ -34,8 +34,8 @@ __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const Kv4Params p) 
         total *= p.h_kv;
         const int tiles = (kv_len + kKv4Tile - 1) / kKv4Tile;
         const long long base = before * p.h_kv + (long long)g * tiles;
-        const int c0 = kv4_cta_of(base, total, p.ctas);
-        n = kv4_cta_of(base + tiles - 1, total, p.ctas) - c0 + 1;
+        const int ctas = kv4_ctas(p, total), c0 = kv4_cta_of(base, total, ctas);
+        n = kv4_cta_of(base + tiles - 1, total, ctas) - c0 + 1;
         if (n == 1) return;  // the output is there already
         first = 2 * (int64_t)c0;
         step = 2;

@@ -247,6 +247,9 @@ struct Kv4Params {
 };
 int kv4_simt_splits(int batch, int h_kv, int rows, int max_kv_len);
 cudaError_t launch_kv4_simt(const Kv4Params &p, cudaStream_t s);
+int kv4_mma_max_rows();  // rows per KV head of the register-expanding tensor-core engine
+int kv4_mma_ctas(int batch, int h_kv, int max_kv_len);
+cudaError_t launch_kv4_mma(const Kv4Params &p, cudaStream_t s);
 cudaError_t launch_kv4_merge(const Kv4Params &p, cudaStream_t s);
 
 }  // namespace sd

@@ -128,7 +128,8 @@ sd_status status_of(cudaError_t e) { return e == cudaSuccess ? SD_OK : SD_ERR_CU
 
 struct Kv4Plan {
     int n_splits, simt_slots;  // CUDA-core engine
-    int ctas;                  // tensor-core engine (0: not for this call)
+    int ctas;                  // tensor-core engines (0: neither serves this call)
+    bool tcgen05;              // which of the two
     size_t ws_bytes;
 };
 
@@ -147,8 +148,10 @@ sd_status plan_kv4(const sd_q_desc *q, const sd_kv4_desc *kv, int batch, Kv4Plan
     *plan = Kv4Plan{};
     plan->n_splits = kv4_simt_splits(batch, kv->h_kv, (int)rows, q->max_kv_len);
     plan->simt_slots = plan->n_splits > 1 ? batch * kv->h_kv * plan->n_splits : 0;
-    if (kv->dtype == SD_BF16 && rows <= kv4_mma_max_rows())
-        plan->ctas = kv4_mma_ctas(batch, kv->h_kv, q->max_kv_len);
+    plan->tcgen05 = rows > kv4_mma_max_rows();
+    if (kv->dtype == SD_BF16 && rows <= kv4_tc_max_rows())
+        plan->ctas = plan->tcgen05 ? kv4_tc_ctas(batch, kv->h_kv, q->max_kv_len)
+                                   : kv4_mma_ctas(batch, kv->h_kv, q->max_kv_len);
     // (whichever engine the pointers' alignment leaves)
     const int slots = plan->simt_slots > 2 * plan->ctas ? plan->simt_slots : 2 * plan->ctas;
     plan->ws_bytes = (size_t)slots * rows * (kv->head_dim + 2) * sizeof(float);
@@ -279,7 +282,8 @@ sd_status sd_kv4_verify_attention(const sd_q_desc *q, const void *q_data, const 
     if (plan.ctas && aligned(q_data, 16) && aligned(out, 16)) {
         p.ctas = plan.ctas;
         p.n_slots = 2 * plan.ctas;
-        return status_of(launch_kv4_mma(p, s));
+        p.wait_ns = wait_limit_ns();
+        return status_of(plan.tcgen05 ? launch_kv4_tc(p, s) : launch_kv4_mma(p, s));
     }
     p.n_splits = plan.n_splits;
     p.n_slots = plan.simt_slots;

@@ -1,0 +1,658 @@
+// tcgen05 attention over a 4-bit cache for many rows per KV head (verification): 17 to 128 rows,
+// bf16.
+//
+// The mathematics is kv4_mma.cu's: scores are products of q with 16 + c, corrected per position
+// by the row's s and lo; V enters as c - 8 with its scale folded into the softmax weights.  With
+// this many rows the products outgrow mma.sync (1,024 products per cycle per SM; a tile of 64 rows
+// would need 2,048 cycles, three times what it takes from HBM), so the codes are expanded to bf16
+// tiles in shared memory once and used by tcgen05.mma (4,096 products per cycle).
+//
+// One persistent CTA per SM, 10 warps; the CTAs share all units' tiles evenly (kv4_common.cuh).
+//   warps 0-3  softmax: TMEM lane r holds MMA row r.  The unit's R rows are placed NCP times
+//              (4 copies up to 32 rows, 2 up to 64, else 1) and each warp handles 128 / NCP
+//              columns of its copy, so a tile's exponentials are spread over all four warps
+//   warps 4-7  expand: each streams 32 positions of every tile (two pages) through its own ring of
+//              cp.async stages and writes them as bf16 into the K and V tiles (128-byte rows of
+//              64 channels, 128-byte swizzle), with the positions' four factors beside them
+//   warp 8     S = Q K^T issuer (Q from TMEM), TMEM owner
+//   warp 9     O += P V issuer (P from TMEM)
+// A word of 8 codes becomes one 16-byte chunk by 4 shifts and 4 and-ors, its channels in the order
+// 0 4 1 5 2 6 3 7; Q is written to TMEM in the same order and O's columns are read back in it, so
+// no code is ever moved to its own place.
+// K and V tiles, S and P are double-buffered: S of tile t overwrites the buffer of tile t - 2
+// once that tile's P V has completed.  Bound by the SM's issue slots and shared memory: a tile's
+// 16 KB of codes become 64 KB written and read again by the tensor core.
+// Every wait on an mbarrier is bounded (see sd_set_wait_timeout_ns); on expiry the CTA records
+// SD_DEVERR_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
+#include "kv4_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace sd {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128;           // MMA M
+constexpr int kTile = kKv4Tile;      // positions per tile
+constexpr int kExpandWarp = 4;       // first of four
+constexpr int kSWarp = 8;
+constexpr int kPvWarp = 9;
+constexpr int kThreads = 10 * 32;
+constexpr int kStages = 4;           // cp.async ring of an expanding warp
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;      // S / P buffers at 0 and 128
+constexpr uint32_t kColQ = 384;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr uint32_t kHalfBytes = kTile * 128;  // 64 channels of a tile
+constexpr int kParSlots = 4;         // tiles whose position factors are kept
+
+template <int D>
+struct TcCfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kRow = D / 2;
+    static constexpr int kCodes = 32 * kRow;               // one warp's share of K (or V)
+    static constexpr int kStageBytes = 2 * kCodes + 256;   // with its parameters
+    static constexpr int kRing = 4 * kTileBytes;           // after K0 K1 V0 V1
+    static constexpr int kPar = kRing + 4 * kStages * kStageBytes;
+    static constexpr int kScratch = kPar + kParSlots * 4 * kTile * 4;
+    // maxima and sums of every MMA row, then 32 columns of the copies' outputs
+    static constexpr int kScratchBytes = (2 * kRows + 96 * 32) * 4;
+    static constexpr int kBars = kScratch + kScratchBytes;
+    static constexpr int kSmem = kBars + 256 + 1024;
+};
+static_assert(TcCfg<128>::kSmem <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ uint32_t pair_at(uint32_t w, int p) {
+    uint32_t x = p == 0 ? w << 3 : w >> (4 * p - 3), r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(0x00780078u), "r"(0x41804180u));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t sub24(uint32_t x) {
+    const __nv_bfloat162 c = __floats2bfloat162_rn(24.f, 24.f);
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), c);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ void copy16z(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4z(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(in ? 4 : 0)
+                 : "memory");
+}
+
+// Column of channel e (0..7) within its group of 8, and the channel order of a group's columns.
+__device__ __forceinline__ constexpr int col_of(int e) { return e < 4 ? 2 * e : 2 * (e - 4) + 1; }
+
+template <int D, int NCP>
+__global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) {
+    pdl_trigger();  // (see launch_pdl)
+    pdl_wait();
+    using C = TcCfg<D>;
+    constexpr unsigned FULL = 0xffffffffu;
+    constexpr int RPC = kRows / NCP;          // rows per copy
+    constexpr int NC = kTile / NCP;           // columns of a softmax warp
+    constexpr int W = NC < 64 ? NC : 64;      // columns held at a time
+    constexpr int kChunks = NC / W;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ long long s_red[2 * kThreads / 32];
+    __shared__ Kv4Start s_start;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    volatile int *abort_flag = &s_abort;
+    uint8_t *sK = smem, *sV = smem + 2 * C::kTileBytes;
+    float *s_par = reinterpret_cast<float *>(smem + C::kPar);
+    const uint32_t bar0 = saddr(smem + C::kBars);
+    auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    // K written, K read (S computed), V written, S computed, P written, P V computed (V read and
+    // the S / P buffer free), per buffer; then a unit's share done, Q written, two drains
+    constexpr int KF = 0, KE = 2, VF = 4, SF = 6, PF = 8, PD = 10, SD = 12, QF = 13, DR = 14, DS = 15;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.group;
+    const int n_active = NCP > 1 ? 4 : min(4, (G * p.max_q_rows + 31) / 32);
+
+    long long lo, hi;
+    const Kv4Cursor first = kv4_first<kThreads>(p, s_red, &s_start, lo, hi);
+    if (hi <= lo) return;
+    const int n_my = (int)(hi - lo);
+    if (warp == kSWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         saddr(&s_tmem)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(BAR(KF + s), 4);
+            mbar_init(BAR(KE + s), 1);
+            mbar_init(BAR(VF + s), 4);
+            mbar_init(BAR(SF + s), 2);  // the commit, and the issuer's own arrival
+            mbar_init(BAR(PF + s), 32 * n_active);
+            mbar_init(BAR(PD + s), 1);
+        }
+        mbar_init(BAR(SD), 1);
+        mbar_init(BAR(QF), 32 * n_active);
+        mbar_init(BAR(DR), 1);
+        mbar_init(BAR(DS), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = s_tmem;
+    // One lane waits; the outcome is the warp's.
+    auto wait1 = [&](int bar, int parity) {
+        bool ok = true;
+        if (lane == 0) ok = mbar_wait(BAR(bar), parity & 1, abort_flag, p.dev_err, p.wait_ns);
+        return __shfl_sync(FULL, ok ? 1 : 0, 0) != 0;
+    };
+
+    if (warp >= kExpandWarp && warp < kExpandWarp + 4) {
+        // ---------------------------------------------------------- copy and expand ----------
+        const int ew = warp - kExpandWarp;
+        const uint32_t ring = saddr(smem + C::kRing) + ew * kStages * C::kStageBytes;
+        const uint8_t *ring_p = smem + C::kRing + ew * kStages * C::kStageBytes;
+        Kv4Cursor pc = first;
+        int copied = 0;
+        int pages[2];
+        auto look_up = [&]() {  // page numbers of the next tile to copy
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = pc.t * kTile + ew * 32 + i * kPageSize;
+                pages[i] = p.page_size && j < pc.kv_len
+                               ? __ldg(p.block_table + (int64_t)pc.b * p.max_pages + (j >> 4))
+                               : 0;
+            }
+        };
+        look_up();
+        auto copy_next = [&]() {
+            if (copied < n_my) {
+                const uint32_t dst = ring + (copied % kStages) * C::kStageBytes;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = pc.t * kTile + ew * 32 + i * kPageSize;
+                    int n = pc.kv_len - j;  // positions (rows past the end are zeros)
+                    int64_t row0 = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h + j;
+                    if (p.page_size) {
+                        row0 = ((int64_t)pages[i] * p.h_kv + pc.g) * kPageSize;
+                        if (n > 0 && (pages[i] < 0 || pages[i] >= p.num_pages)) {
+                            if (lane == 0) set_dev_err(p.dev_err, SD_DEVERR_PAGE);
+                            n = 0;
+                        }
+                    }
+                    if (n <= 0) row0 = 0;
+                    constexpr int Q = C::kRow / 16;  // 16-byte chunks of a row
+#pragma unroll
+                    for (int k = 0; k < kPageSize * Q / 32; ++k) {
+                        const int x = lane + 32 * k, r = x / Q, q = x % Q;
+                        const bool in = r < n;
+                        const int64_t off = (row0 + (in ? r : 0)) * C::kRow + q * 16;
+                        // chunk q of row r at q ^ (r/2 mod Q): 8 rows' chunks in different banks
+                        const int rr = i * kPageSize + r;
+                        const uint32_t at = dst + rr * C::kRow + ((q ^ ((rr / (8 / Q)) % Q)) << 4);
+                        copy16z(at, p.k + off, in);
+                        copy16z(at + C::kCodes, p.v + off, in);
+                    }
+                    const int r = lane & 15;
+                    const bool in = r < n;
+                    copy4z(dst + 2 * C::kCodes + (lane & 16) * 8 + (i * kPageSize + r) * 4,
+                           (lane < 16 ? p.kp : p.vp) + row0 + (in ? r : 0), in);
+                }
+                ++copied;
+                pc.next(p);
+                if (copied < n_my) look_up();
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) copy_next();
+        constexpr int Q = C::kRow / 16;
+        // lane: row (lane & 15) of a page, chunks (lane >> 4), (lane >> 4) + 2, ...
+        auto expand = [&](const uint8_t *src, uint8_t *dst, auto &&f) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int rr = i * kPageSize + (lane & 15), row = ew * 32 + rr;
+#pragma unroll
+                for (int k = 0; k < Q / 2; ++k) {
+                    const int q = 2 * k + (lane >> 4);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(
+                        src + rr * C::kRow + ((q ^ ((rr / (8 / Q)) % Q)) << 4));
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int slot = 4 * q + c;  // 8 channels: 16-byte chunk of the bf16 row
+                        *reinterpret_cast<uint4 *>(dst + (slot >> 3) * kHalfBytes + row * 128 +
+                                                   (((slot & 7) ^ (row & 7)) << 4)) =
+                            make_uint4(f(pair_at(w[c], 0)), f(pair_at(w[c], 1)),
+                                       f(pair_at(w[c], 2)), f(pair_at(w[c], 3)));
+                    }
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+        };
+        for (int t = 0; t < n_my; ++t) {
+            const int s = t & 1;
+            copy_next();
+            cp_async_wait<kStages - 1>();
+            __syncwarp();
+            const uint8_t *st = ring_p + (t % kStages) * C::kStageBytes;
+            if (t >= 2 && !wait1(KE + s, (t - 2) >> 1)) break;
+            {
+                // Factors of this lane's position.  (Slot t % 4: the softmax of tile t - 4 is
+                // past it, since S of tile t - 2 has completed and that waited for the P V of
+                // tile t - 4.)
+                const uint32_t *par = reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes);
+                const uint32_t kp = par[lane], vp = par[32 + lane];
+                float *d = s_par + (t % kParSlots) * 4 * kTile + ew * 32 + lane;
+                const float ks = param_scale(kp) * p.scale_log2, vs = param_scale(vp);
+                d[0] = ks;
+                d[kTile] = fmaf(param_low(kp), p.scale_log2, -16.f * ks);
+                d[2 * kTile] = vs;
+                d[3 * kTile] = fmaf(8.f, vs, param_low(vp));
+            }
+            expand(st, sK + s * C::kTileBytes, [](uint32_t x) { return x; });
+            if (lane == 0) mbar_arrive(BAR(KF + s));
+            if (t >= 2 && !wait1(PD + s, (t - 2) >> 1)) break;
+            expand(st + C::kCodes, sV + s * C::kTileBytes, [](uint32_t x) { return sub24(x); });
+            if (lane == 0) mbar_arrive(BAR(VF + s));
+        }
+        cp_async_wait<0>();
+    } else if (warp == kSWarp) {
+        // ---------------------------------------------------------- S = Q K^T issuer ---------
+        const uint32_t idesc = idesc_bf16(kTile, false);
+        bool issued = false;
+        Kv4Cursor c = first;
+        int seg = 0;
+        for (int t = 0; t < n_my; ++t) {
+            const int s = t & 1;
+            bool ok = true;
+            if (t == 0 || c.t == 0) ok = wait1(QF, seg++);  // a unit's share begins
+            ok = ok && wait1(KF + s, t >> 1) && (t < 2 || wait1(PD + s, (t - 2) >> 1));
+            if (!ok) break;
+            tc_after();
+            if (lane == 0) {
+                const uint32_t kb = saddr(sK + s * C::kTileBytes);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ts(tmem + s * kTile, tmem + kColQ + kk * 8,
+                           desc_k_sw128(kb + (kk >> 2) * kHalfBytes + (kk & 3) * 32), idesc,
+                           kk > 0 ? 1u : 0u);
+                mma_commit(BAR(SF + s));
+                mma_commit(BAR(KE + s));
+                mbar_arrive(BAR(SF + s));  // (orders the factors before the softmax's reads)
+                issued = true;
+            }
+            __syncwarp();
+            c.next(p);
+        }
+        const bool any = __any_sync(FULL, issued);
+        if (lane == 0 && any) {
+            mma_commit(BAR(DS));
+            const unsigned long long t0 = now_ns();
+            while (!mbar_try(BAR(DS), 0) && now_ns() - t0 < kDrainNs) {
+            }
+        }
+        __syncwarp();
+    } else if (warp == kPvWarp) {
+        // ---------------------------------------------------------- O += P V issuer ----------
+        const uint32_t idesc = idesc_bf16(D, true);
+        bool issued = false;
+        Kv4Cursor c = first;
+        for (int t = 0; t < n_my; ++t) {
+            const int s = t & 1;
+            if (!(wait1(PF + s, t >> 1) && wait1(VF + s, t >> 1))) break;
+            tc_after();
+            const bool fresh = t == 0 || c.t == 0;
+            const bool last = t + 1 == n_my || c.t + 1 == c.tiles;
+            if (lane == 0) {
+                const uint32_t vb = saddr(sV + s * C::kTileBytes);
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    mma_ts(tmem + kColO, tmem + s * kTile + kk * 8,
+                           desc_mn_sw128(vb + kk * 2048, kHalfBytes), idesc,
+                           (!fresh || kk > 0) ? 1u : 0u);
+                mma_commit(BAR(PD + s));
+                if (last) mma_commit(BAR(SD));
+                issued = true;
+            }
+            __syncwarp();
+            c.next(p);
+        }
+        const bool any = __any_sync(FULL, issued);
+        if (lane == 0 && any) {
+            mma_commit(BAR(DR));
+            const unsigned long long t0 = now_ns();
+            while (!mbar_try(BAR(DR), 0) && now_ns() - t0 < kDrainNs) {
+            }
+        }
+        __syncwarp();
+    } else if (warp < n_active) {
+        // ---------------------------------------------------------- softmax -------------------
+        // tcgen05.ld / st are warp-collective: every lane executes them and decisions that gate
+        // them are made uniform by votes.
+        const int cp = NCP > 1 ? warp / (4 / NCP) : 0;  // this warp's row copy
+        const int c0 = cp * NC;                         // its first column
+        const int r = warp * 32 + lane - cp * RPC;      // its row
+        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        float *s_m = reinterpret_cast<float *>(smem + C::kScratch), *s_l = s_m + kRows;
+        float4 *s_o = reinterpret_cast<float4 *>(s_l + kRows);  // [copy - 1][RPC][8]
+        // Q of unit u into TMEM (zeros past its rows), channels of each group of 8 in the order of
+        // the expanded codes; returns the row's sum.
+        auto write_q = [&](const Kv4Cursor &u) {
+            const bool has = r < u.n_q * G;
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                static_cast<const unsigned short *>(p.q) +
+                ((int64_t)(u.q0 + (has ? r / G : 0)) * p.h_q + u.g * G + (has ? r % G : 0)) * D);
+            float sum = 0.f;
+#pragma unroll
+            for (int hh = 0; hh < D / 64; ++hh) {
+                float qf[32];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 x = has ? __ldg(src + hh * 8 + c) : make_uint4(0u, 0u, 0u, 0u);
+                    qf[4 * c] = __uint_as_float(__byte_perm(x.x, x.z, 0x5410));
+                    qf[4 * c + 1] = __uint_as_float(__byte_perm(x.x, x.z, 0x7632));
+                    qf[4 * c + 2] = __uint_as_float(__byte_perm(x.y, x.w, 0x5410));
+                    qf[4 * c + 3] = __uint_as_float(__byte_perm(x.y, x.w, 0x7632));
+                    sum += (bf16_lo(x.x) + bf16_hi(x.x)) + (bf16_lo(x.y) + bf16_hi(x.y)) +
+                           ((bf16_lo(x.z) + bf16_hi(x.z)) + (bf16_lo(x.w) + bf16_hi(x.w)));
+                }
+                tmem_st32(lane_base + kColQ + hh * 32, qf);
+            }
+            tc_before();
+            mbar_arrive(BAR(QF));
+            return sum;
+        };
+        Kv4Cursor u = first;
+        float qsum = write_q(u);
+        bool ok_run = true;
+        int t = 0, seg = 0;
+        while (t < n_my) {
+            const int n_seg = min(u.tiles - u.t, n_my - t);
+            const bool starts = u.t == 0, ends = u.t + n_seg == u.tiles;
+            const int R = u.n_q * G;
+            const bool row_ok = r < R;
+            const int limit = row_ok ? u.kv_len - u.n_q + r / G : -1;
+            const int first_limit = u.kv_len - u.n_q;
+            float m = -INFINITY;
+            float2 l2 = make_float2(0.f, 0.f), cr2 = make_float2(0.f, 0.f);
+            const float2 qs2 = make_float2(qsum, qsum);
+            const int t_end = t + n_seg;
+            for (int lt = u.t; ok_run && t < t_end; ++t, ++lt) {
+                const int s = t & 1;
+                const bool got =
+                    mbar_wait(BAR(SF + s), (t >> 1) & 1, abort_flag, p.dev_err, p.wait_ns);
+                if (!__all_sync(FULL, got)) {
+                    ok_run = false;
+                    break;
+                }
+                tc_after();
+                const uint32_t s_addr = lane_base + s * kTile;
+                const float *par = s_par + (t % kParSlots) * 4 * kTile;
+                const int p0 = lt * kTile;
+                // every row sees every position of the tile (rows past R may compute anything)
+                const bool interior = p0 + kTile - 1 <= first_limit;
+                float v[W];
+                // scores of columns [cb, cb + W) in log2 units
+                auto scores = [&](int cb) {
+                    tmem_ld_cols<W>(s_addr + cb, v);
+                    const float4 *ks = reinterpret_cast<const float4 *>(par + cb);
+                    const float4 *kl = reinterpret_cast<const float4 *>(par + kTile + cb);
+#pragma unroll
+                    for (int e = 0; e < W; e += 4) {
+                        const float4 a = ks[e / 4], b = kl[e / 4];
+                        const float2 x = __ffma2_rn(make_float2(v[e], v[e + 1]), make_float2(a.x, a.y),
+                                                    __fmul2_rn(make_float2(b.x, b.y), qs2));
+                        const float2 y =
+                            __ffma2_rn(make_float2(v[e + 2], v[e + 3]), make_float2(a.z, a.w),
+                                       __fmul2_rn(make_float2(b.z, b.w), qs2));
+                        v[e] = x.x;
+                        v[e + 1] = x.y;
+                        v[e + 2] = y.x;
+                        v[e + 3] = y.y;
+                    }
+                    if (!interior) {
+#pragma unroll
+                        for (int e = 0; e < W; ++e)
+                            if (p0 + cb + e > limit) v[e] = -INFINITY;
+                    }
+                };
+                float mx = -INFINITY;
+#pragma unroll
+                for (int ch = 0; ch < kChunks; ++ch) {
+                    scores(c0 + ch * W);
+#pragma unroll
+                    for (int e = 0; e < W; e += 2) mx = max3(mx, v[e], v[e + 1]);
+                }
+                const bool grow = mx > m + kRescaleLog2;
+                const bool rescale = grow && m != -INFINITY;
+                if (__any_sync(FULL, rescale)) {
+                    // O holds the share's tiles before t: wait for the P V of tile t - 1.  (Its
+                    // barrier is in phase t - 3 or t - 1: S of tile t - 1 waited for the former,
+                    // and tile t + 1's P V needs this warp's arrival.)
+                    const bool done = mbar_wait(BAR(PD + ((t - 1) & 1)), ((t - 1) >> 1) & 1,
+                                                abort_flag, p.dev_err, p.wait_ns);
+                    if (!__all_sync(FULL, done)) {
+                        ok_run = false;
+                        break;
+                    }
+                    tc_after();
+                    const float f = rescale ? ex2(m - mx) : 1.f;
+                    float o[32];
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        tmem_ld32(lane_base + kColO + c * 32, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= f;
+                        tmem_st32(lane_base + kColO + c * 32, o);
+                    }
+                    l2.x *= f;
+                    l2.y *= f;
+                    cr2.x *= f;
+                    cr2.y *= f;
+                }
+                if (grow) m = mx;
+                const float nm = m == -INFINITY ? 0.f : -m;
+                const float2 nm2 = make_float2(nm, nm);
+                uint32_t pk[NC / 2];
+#pragma unroll
+                for (int ch = 0; ch < kChunks; ++ch) {
+                    const int cb = c0 + ch * W;
+                    if (kChunks > 1) scores(cb);
+                    const float4 *vs = reinterpret_cast<const float4 *>(par + 2 * kTile + cb);
+                    const float4 *vl = reinterpret_cast<const float4 *>(par + 3 * kTile + cb);
+#pragma unroll
+                    for (int e = 0; e < W; e += 4) {
+                        const float4 a = vs[e / 4], b = vl[e / 4];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float2 x = make_float2(v[e + 2 * h], v[e + 2 * h + 1]);
+                            float2 s2 = h ? make_float2(a.z, a.w) : make_float2(a.x, a.y);
+                            float2 b2 = h ? make_float2(b.z, b.w) : make_float2(b.x, b.y);
+                            if (!interior) {  // a hidden position's NaN must not get through
+                                if (x.x == -INFINITY) s2.x = b2.x = 0.f;
+                                if (x.y == -INFINITY) s2.y = b2.y = 0.f;
+                            }
+                            const float2 d = __fadd2_rn(x, nm2);
+                            const float2 pe = make_float2(ex2(d.x), ex2(d.y));
+                            l2 = __fadd2_rn(l2, pe);
+                            cr2 = __ffma2_rn(pe, b2, cr2);
+                            const float2 w = __fmul2_rn(pe, s2);
+                            pk[(ch * W + e) / 2 + h] = pack_bf16(w.x, w.y);
+                        }
+                    }
+                }
+                // P over S: this copy's columns at c0 / 2, zeros in the other copies'
+                if constexpr (NCP == 1) {
+                    tmem_st64(s_addr, pk);
+                } else {
+                    uint32_t prow[kTile / 2];
+#pragma unroll
+                    for (int i = 0; i < kTile / 2; ++i) prow[i] = 0u;
+#pragma unroll
+                    for (int q = 0; q < NCP; ++q)
+                        if (q == cp)
+#pragma unroll
+                            for (int i = 0; i < NC / 2; ++i) prow[q * (NC / 2) + i] = pk[i];
+                    tmem_st64(s_addr, prow);
+                }
+                tc_before();
+                mbar_arrive(BAR(PF + s));
+            }
+            t = t_end;  // (after a failed wait every warp still passes the barriers below)
+            // ---- end of the share: the next one's Q, then this one's output ----
+            Kv4Cursor nx = u;
+            nx.skip(p, n_seg);
+            if (ok_run && t < n_my) qsum = write_q(nx);
+            bool done = ok_run;
+            if (ok_run) done = mbar_wait(BAR(SD), seg & 1, abort_flag, p.dev_err, p.wait_ns);
+            ++seg;
+            const bool read_o = __all_sync(FULL, done);
+            if (!read_o) ok_run = false;
+            tc_after();
+            float l = l2.x + l2.y, cr = cr2.x + cr2.y;
+            if (l != l && m == -INFINITY) m = 0.f;  // (a NaN sum survives the merges)
+            float fq[NCP];
+            if constexpr (NCP > 1) {
+                asm volatile("bar.sync 1, 128;" ::: "memory");  // the last share's merge is done
+                s_m[cp * RPC + r] = m;
+                s_l[cp * RPC + r] = l;
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (cp == 0) {
+                    float M = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < NCP; ++q) M = fmaxf(M, s_m[q * RPC + r]);
+                    l = 0.f;
+#pragma unroll
+                    for (int q = 0; q < NCP; ++q) {
+                        const float mq = s_m[q * RPC + r];
+                        fq[q] = mq == -INFINITY ? 0.f : ex2(mq - M);
+                        l += fq[q] * s_l[q * RPC + r];
+                    }
+                    m = M;
+                }
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int row = u.q0 + (row_ok ? r / G : 0), h = u.g * G + (row_ok ? r % G : 0);
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                if (read_o) tmem_ld32(lane_base + kColO + c * 32, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] += cr;
+                if constexpr (NCP > 1) {
+                    // copies 1.. pass their 32 columns through shared memory (16-byte chunk k of
+                    // row r in slot k ^ (r & 7))
+                    if (cp > 0) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            s_o[((cp - 1) * RPC + r) * 8 + (k ^ (r & 7))] =
+                                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    }
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (cp == 0) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float4 a = make_float4(fq[0] * o[4 * k], fq[0] * o[4 * k + 1],
+                                                   fq[0] * o[4 * k + 2], fq[0] * o[4 * k + 3]);
+#pragma unroll
+                            for (int q = 1; q < NCP; ++q) {
+                                const float4 x = s_o[((q - 1) * RPC + r) * 8 + (k ^ (r & 7))];
+                                a.x = fmaf(fq[q], x.x, a.x);
+                                a.y = fmaf(fq[q], x.y, a.y);
+                                a.z = fmaf(fq[q], x.z, a.z);
+                                a.w = fmaf(fq[q], x.w, a.w);
+                            }
+                            o[4 * k] = a.x;
+                            o[4 * k + 1] = a.y;
+                            o[4 * k + 2] = a.z;
+                            o[4 * k + 3] = a.w;
+                        }
+                    }
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                }
+                if (!row_ok || cp != 0 || !read_o) continue;
+                // columns to channels: group of 8 by group of 8
+                if (starts && ends) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<unsigned short *>(p.out) +
+                                                           ((int64_t)row * p.h_q + h) * D + c * 32);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float *x = o + 8 * k;
+                        dst[k] = make_uint4(
+                            pack_bf16(x[col_of(0)] * inv, x[col_of(1)] * inv),
+                            pack_bf16(x[col_of(2)] * inv, x[col_of(3)] * inv),
+                            pack_bf16(x[col_of(4)] * inv, x[col_of(5)] * inv),
+                            pack_bf16(x[col_of(6)] * inv, x[col_of(7)] * inv));
+                    }
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(kv4_slot_o(p, slot, r) + c * 32);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float *x = o + 8 * k;
+                        dst[2 * k] = make_float4(x[col_of(0)], x[col_of(1)], x[col_of(2)], x[col_of(3)]);
+                        dst[2 * k + 1] =
+                            make_float4(x[col_of(4)], x[col_of(5)], x[col_of(6)], x[col_of(7)]);
+                    }
+                    if (c == 0) {
+                        float *ml = kv4_slot_ml(p, slot, r);
+                        ml[0] = m;
+                        ml[1] = l;
+                    }
+                }
+            }
+            u = nx;
+        }
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == kSWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kTmemCols)
+                     : "memory");
+}
+
+template <int D, int NCP>
+cudaError_t launch_t(const Kv4Params &p, cudaStream_t s) {
+    constexpr int bytes = TcCfg<D>::kSmem;
+    cudaError_t e = set_max_dynamic_smem<kv4_tc_kernel<D, NCP>>(bytes);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kv4_tc_kernel<D, NCP>, dim3(p.ctas), dim3(kThreads), bytes, s, p);
+    return e != cudaSuccess ? e : launch_kv4_merge(p, s);
+}
+
+template <int D>
+cudaError_t launch_d(const Kv4Params &p, cudaStream_t s) {
+    const int rows = p.group * p.max_q_rows;
+    return rows <= 32 ? launch_t<D, 4>(p, s) : rows <= 64 ? launch_t<D, 2>(p, s) : launch_t<D, 1>(p, s);
+}
+
+}  // namespace
+
+int kv4_tc_max_rows() { return kRows; }
+
+int kv4_tc_ctas(int batch, int h_kv, int max_kv_len) {
+    const long long tiles = (long long)batch * h_kv * (((long long)max_kv_len + kTile - 1) / kTile);
+    const int sms = device_sm_count();
+    return (int)(tiles < sms ? tiles : sms);
+}
+
+cudaError_t launch_kv4_tc(const Kv4Params &p, cudaStream_t s) {
+    return p.head_dim == 128 ? launch_d<128>(p, s) : launch_d<64>(p, s);
+}
+
+}  // namespace sd

@@ -244,12 +244,16 @@ struct Kv4Params {
     int n_slots;     // partial results that ws holds, [n_slots][group * max_q_rows] rows each
     float *ws;
     int32_t *dev_err;
+    unsigned long long wait_ns;  // bound of every pipeline wait inside the tcgen05 kernel
 };
 int kv4_simt_splits(int batch, int h_kv, int rows, int max_kv_len);
 cudaError_t launch_kv4_simt(const Kv4Params &p, cudaStream_t s);
 int kv4_mma_max_rows();  // rows per KV head of the register-expanding tensor-core engine
 int kv4_mma_ctas(int batch, int h_kv, int max_kv_len);
 cudaError_t launch_kv4_mma(const Kv4Params &p, cudaStream_t s);
+int kv4_tc_max_rows();  // rows per KV head of the tcgen05 engine
+int kv4_tc_ctas(int batch, int h_kv, int max_kv_len);
+cudaError_t launch_kv4_tc(const Kv4Params &p, cudaStream_t s);
 cudaError_t launch_kv4_merge(const Kv4Params &p, cudaStream_t s);
 
 }  // namespace sd

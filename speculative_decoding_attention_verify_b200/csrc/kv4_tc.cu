@@ -7,18 +7,25 @@
 // would need 2,048 cycles, three times what it takes from HBM), so the codes are expanded to bf16
 // tiles in shared memory once and used by tcgen05.mma (4,096 products per cycle).
 //
-// One persistent CTA per SM, 10 warps; the CTAs share all units' tiles evenly (kv4_common.cuh).
+// One persistent CTA per SM, 14 warps; the CTAs share all units' tiles evenly (kv4_common.cuh).
 //   warps 0-3  softmax: TMEM lane r holds MMA row r.  The unit's R rows are placed NCP times
 //              (4 copies up to 32 rows, 2 up to 64, else 1) and each warp handles 128 / NCP
 //              columns of its copy, so a tile's exponentials are spread over all four warps
-//   warps 4-7  expand: each streams 32 positions of every tile (two pages) through its own ring of
+//   warps 4-11 expand: each streams 16 positions of every tile (a page) through its own ring of
 //              cp.async stages and writes them as bf16 into the K and V tiles (128-byte rows of
 //              64 channels, 128-byte swizzle), with the positions' four factors beside them
-//   warp 8     S = Q K^T issuer (Q from TMEM), TMEM owner
-//   warp 9     O += P V issuer (P from TMEM)
+//   warp 12    S = Q K^T issuer (Q from TMEM), TMEM owner
+//   warp 13    O += P V issuer (P from TMEM)
 // A word of 8 codes becomes one 16-byte chunk by 4 shifts and 4 and-ors, its channels in the order
 // 0 4 1 5 2 6 3 7; Q is written to TMEM in the same order and O's columns are read back in it, so
 // no code is ever moved to its own place.
+// The softmax takes 32 columns at a time in one pass: the exponents are taken from the running
+// maximum as it stands, and only when one exceeds it by more than 2^16 does the maximum move
+// (then O, the sums and the tile's earlier weights are rescaled; weights stay finite in bf16 far
+// beyond that).  A second pass, or a tile's columns unrolled into one block of code, costs more
+// than its instructions: the warps' roles together must stay within the instruction cache (with
+// 64 columns and 32 positions unrolled, two of three issue slots were lost to instruction fetch
+// and a tile took 7,000 cycles).
 // K and V tiles, S and P are double-buffered: S of tile t overwrites the buffer of tile t - 2
 // once that tile's P V has completed.  Bound by the SM's issue slots and shared memory: a tile's
 // 16 KB of codes become 64 KB written and read again by the tensor core.
@@ -34,27 +41,28 @@ using namespace tc;
 
 constexpr int kRows = 128;           // MMA M
 constexpr int kTile = kKv4Tile;      // positions per tile
-constexpr int kExpandWarp = 4;       // first of four
-constexpr int kSWarp = 8;
-constexpr int kPvWarp = 9;
-constexpr int kThreads = 10 * 32;
+constexpr int kExpandWarp = 4;       // first of eight
+constexpr int kExpandWarps = 8;
+constexpr int kSWarp = 12;
+constexpr int kPvWarp = 13;
+constexpr int kThreads = 14 * 32;
+static_assert(kExpandWarps * kPageSize == kTile, "a page per expanding warp");
 constexpr int kStages = 4;           // cp.async ring of an expanding warp
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;      // S / P buffers at 0 and 128
 constexpr uint32_t kColQ = 384;
-constexpr float kRescaleLog2 = 8.0f;
+constexpr float kRescaleLog2 = 16.0f;
 constexpr uint32_t kHalfBytes = kTile * 128;  // 64 channels of a tile
 constexpr int kParSlots = 4;         // tiles whose position factors are kept
 
 template <int D>
 struct TcCfg {
-    static constexpr int kHalves = D / 64;
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kRow = D / 2;
-    static constexpr int kCodes = 32 * kRow;               // one warp's share of K (or V)
-    static constexpr int kStageBytes = 2 * kCodes + 256;   // with its parameters
+    static constexpr int kCodes = kPageSize * kRow;        // one warp's share of K (or V)
+    static constexpr int kStageBytes = 2 * kCodes + 128;   // with its parameters
     static constexpr int kRing = 4 * kTileBytes;           // after K0 K1 V0 V1
-    static constexpr int kPar = kRing + 4 * kStages * kStageBytes;
+    static constexpr int kPar = kRing + kExpandWarps * kStages * kStageBytes;
     static constexpr int kScratch = kPar + kParSlots * 4 * kTile * 4;
     // maxima and sums of every MMA row, then 32 columns of the copies' outputs
     static constexpr int kScratchBytes = (2 * kRows + 96 * 32) * 4;
@@ -86,6 +94,29 @@ __device__ __forceinline__ void copy4z(uint32_t dst, const void *src, bool in) {
                  : "memory");
 }
 
+// 16 consecutive columns of this thread's TMEM lane.  The store is not waited for: a wait::st comes
+// before the columns are loaded again or handed to the tensor core.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 // Column of channel e (0..7) within its group of 8, and the channel order of a group's columns.
 __device__ __forceinline__ constexpr int col_of(int e) { return e < 4 ? 2 * e : 2 * (e - 4) + 1; }
 
@@ -97,8 +128,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
     constexpr unsigned FULL = 0xffffffffu;
     constexpr int RPC = kRows / NCP;          // rows per copy
     constexpr int NC = kTile / NCP;           // columns of a softmax warp
-    constexpr int W = NC < 64 ? NC : 64;      // columns held at a time
-    constexpr int kChunks = NC / W;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -131,9 +160,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
     }
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(BAR(KF + s), 4);
+            mbar_init(BAR(KF + s), kExpandWarps);
             mbar_init(BAR(KE + s), 1);
-            mbar_init(BAR(VF + s), 4);
+            mbar_init(BAR(VF + s), kExpandWarps);
             mbar_init(BAR(SF + s), 2);  // the commit, and the issuer's own arrival
             mbar_init(BAR(PF + s), 32 * n_active);
             mbar_init(BAR(PD + s), 1);
@@ -156,57 +185,49 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
         return __shfl_sync(FULL, ok ? 1 : 0, 0) != 0;
     };
 
-    if (warp >= kExpandWarp && warp < kExpandWarp + 4) {
+    if (warp >= kExpandWarp && warp < kExpandWarp + kExpandWarps) {
         // ---------------------------------------------------------- copy and expand ----------
         const int ew = warp - kExpandWarp;
         const uint32_t ring = saddr(smem + C::kRing) + ew * kStages * C::kStageBytes;
         const uint8_t *ring_p = smem + C::kRing + ew * kStages * C::kStageBytes;
         Kv4Cursor pc = first;
-        int copied = 0;
-        int pages[2];
-        auto look_up = [&]() {  // page numbers of the next tile to copy
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int j = pc.t * kTile + ew * 32 + i * kPageSize;
-                pages[i] = p.page_size && j < pc.kv_len
-                               ? __ldg(p.block_table + (int64_t)pc.b * p.max_pages + (j >> 4))
-                               : 0;
-            }
+        int copied = 0, page;
+        auto look_up = [&]() {  // page of the next tile to copy
+            const int j = pc.t * kTile + ew * kPageSize;
+            page = p.page_size && j < pc.kv_len
+                       ? __ldg(p.block_table + (int64_t)pc.b * p.max_pages + (j >> 4))
+                       : 0;
         };
         look_up();
+        constexpr int Q = C::kRow / 16;  // 16-byte chunks of a row
+        // chunk q of row r is kept at q ^ (r / (8 / Q) mod Q): 8 rows' chunks in different banks
+        auto raw_at = [](int r, int q) { return r * C::kRow + ((q ^ ((r / (8 / Q)) % Q)) << 4); };
         auto copy_next = [&]() {
             if (copied < n_my) {
                 const uint32_t dst = ring + (copied % kStages) * C::kStageBytes;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = pc.t * kTile + ew * 32 + i * kPageSize;
-                    int n = pc.kv_len - j;  // positions (rows past the end are zeros)
-                    int64_t row0 = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h + j;
-                    if (p.page_size) {
-                        row0 = ((int64_t)pages[i] * p.h_kv + pc.g) * kPageSize;
-                        if (n > 0 && (pages[i] < 0 || pages[i] >= p.num_pages)) {
-                            if (lane == 0) set_dev_err(p.dev_err, SD_DEVERR_PAGE);
-                            n = 0;
-                        }
+                const int j = pc.t * kTile + ew * kPageSize;
+                int n = pc.kv_len - j;  // positions (rows past the end are zeros)
+                int64_t row0 = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h + j;
+                if (p.page_size) {
+                    row0 = ((int64_t)page * p.h_kv + pc.g) * kPageSize;
+                    if (n > 0 && (page < 0 || page >= p.num_pages)) {
+                        if (lane == 0) set_dev_err(p.dev_err, SD_DEVERR_PAGE);
+                        n = 0;
                     }
-                    if (n <= 0) row0 = 0;
-                    constexpr int Q = C::kRow / 16;  // 16-byte chunks of a row
-#pragma unroll
-                    for (int k = 0; k < kPageSize * Q / 32; ++k) {
-                        const int x = lane + 32 * k, r = x / Q, q = x % Q;
-                        const bool in = r < n;
-                        const int64_t off = (row0 + (in ? r : 0)) * C::kRow + q * 16;
-                        // chunk q of row r at q ^ (r/2 mod Q): 8 rows' chunks in different banks
-                        const int rr = i * kPageSize + r;
-                        const uint32_t at = dst + rr * C::kRow + ((q ^ ((rr / (8 / Q)) % Q)) << 4);
-                        copy16z(at, p.k + off, in);
-                        copy16z(at + C::kCodes, p.v + off, in);
-                    }
-                    const int r = lane & 15;
-                    const bool in = r < n;
-                    copy4z(dst + 2 * C::kCodes + (lane & 16) * 8 + (i * kPageSize + r) * 4,
-                           (lane < 16 ? p.kp : p.vp) + row0 + (in ? r : 0), in);
                 }
+                if (n <= 0) row0 = 0;
+#pragma unroll
+                for (int k = 0; k < kPageSize * Q / 32; ++k) {
+                    const int x = lane + 32 * k, r = x / Q, q = x % Q;
+                    const bool in = r < n;
+                    const int64_t off = (row0 + (in ? r : 0)) * C::kRow + q * 16;
+                    copy16z(dst + raw_at(r, q), p.k + off, in);
+                    copy16z(dst + C::kCodes + raw_at(r, q), p.v + off, in);
+                }
+                const int r = lane & 15;
+                const bool in = r < n;
+                copy4z(dst + 2 * C::kCodes + lane * 4,
+                       (lane < 16 ? p.kp : p.vp) + row0 + (in ? r : 0), in);
                 ++copied;
                 pc.next(p);
                 if (copied < n_my) look_up();
@@ -215,26 +236,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
         };
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) copy_next();
-        constexpr int Q = C::kRow / 16;
-        // lane: row (lane & 15) of a page, chunks (lane >> 4), (lane >> 4) + 2, ...
+        // lane: row (lane & 15), chunks (lane >> 4), (lane >> 4) + 2
         auto expand = [&](const uint8_t *src, uint8_t *dst, auto &&f) {
+            const int r = lane & 15, row = ew * kPageSize + r;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int rr = i * kPageSize + (lane & 15), row = ew * 32 + rr;
+            for (int k = 0; k < Q / 2; ++k) {
+                const int q = 2 * k + (lane >> 4);
+                const uint4 x = *reinterpret_cast<const uint4 *>(src + raw_at(r, q));
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int k = 0; k < Q / 2; ++k) {
-                    const int q = 2 * k + (lane >> 4);
-                    const uint4 x = *reinterpret_cast<const uint4 *>(
-                        src + rr * C::kRow + ((q ^ ((rr / (8 / Q)) % Q)) << 4));
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int slot = 4 * q + c;  // 8 channels: 16-byte chunk of the bf16 row
-                        *reinterpret_cast<uint4 *>(dst + (slot >> 3) * kHalfBytes + row * 128 +
-                                                   (((slot & 7) ^ (row & 7)) << 4)) =
-                            make_uint4(f(pair_at(w[c], 0)), f(pair_at(w[c], 1)),
-                                       f(pair_at(w[c], 2)), f(pair_at(w[c], 3)));
-                    }
+                for (int c = 0; c < 4; ++c) {
+                    const int slot = 4 * q + c;  // 8 channels: 16-byte chunk of the bf16 row
+                    *reinterpret_cast<uint4 *>(dst + (slot >> 3) * kHalfBytes + row * 128 +
+                                               (((slot & 7) ^ (row & 7)) << 4)) =
+                        make_uint4(f(pair_at(w[c], 0)), f(pair_at(w[c], 1)), f(pair_at(w[c], 2)),
+                                   f(pair_at(w[c], 3)));
                 }
             }
             fence_async_smem();
@@ -252,13 +268,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
                 // past it, since S of tile t - 2 has completed and that waited for the P V of
                 // tile t - 4.)
                 const uint32_t *par = reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes);
-                const uint32_t kp = par[lane], vp = par[32 + lane];
-                float *d = s_par + (t % kParSlots) * 4 * kTile + ew * 32 + lane;
-                const float ks = param_scale(kp) * p.scale_log2, vs = param_scale(vp);
-                d[0] = ks;
-                d[kTile] = fmaf(param_low(kp), p.scale_log2, -16.f * ks);
-                d[2 * kTile] = vs;
-                d[3 * kTile] = fmaf(8.f, vs, param_low(vp));
+                // (lanes 0-15 the key's two, lanes 16-31 the value's)
+                const uint32_t w = par[lane];
+                float *d = s_par + (t % kParSlots) * 4 * kTile + (lane >> 4) * 2 * kTile +
+                           ew * kPageSize + (lane & 15);
+                const float sc = param_scale(w), lw = param_low(w);
+                const float a = lane < 16 ? sc * p.scale_log2 : sc;
+                d[0] = a;
+                d[kTile] = lane < 16 ? fmaf(lw, p.scale_log2, -16.f * a) : fmaf(8.f, a, lw);
             }
             expand(st, sK + s * C::kTileBytes, [](uint32_t x) { return x; });
             if (lane == 0) mbar_arrive(BAR(KF + s));
@@ -384,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
             const bool row_ok = r < R;
             const int limit = row_ok ? u.kv_len - u.n_q + r / G : -1;
             const int first_limit = u.kv_len - u.n_q;
-            float m = -INFINITY;
+            float m = -INFINITY, nm = 0.f;
+            const int seg_lo = u.t;
             float2 l2 = make_float2(0.f, 0.f), cr2 = make_float2(0.f, 0.f);
             const float2 qs2 = make_float2(qsum, qsum);
             const int t_end = t + n_seg;
@@ -402,20 +420,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
                 const int p0 = lt * kTile;
                 // every row sees every position of the tile (rows past R may compute anything)
                 const bool interior = p0 + kTile - 1 <= first_limit;
-                float v[W];
-                // scores of columns [cb, cb + W) in log2 units
-                auto scores = [&](int cb) {
-                    tmem_ld_cols<W>(s_addr + cb, v);
+#pragma unroll 1
+                for (int ch = 0; ch < NC / 32; ++ch) {
+                    const int cb = c0 + ch * 32;
+                    float v[32];
+                    tmem_ld32(s_addr + cb, v);
+                    // exponents of the weights: the scores in log2 units less the maximum
                     const float4 *ks = reinterpret_cast<const float4 *>(par + cb);
                     const float4 *kl = reinterpret_cast<const float4 *>(par + kTile + cb);
+                    const float2 nm2 = make_float2(nm, nm);
 #pragma unroll
-                    for (int e = 0; e < W; e += 4) {
+                    for (int e = 0; e < 32; e += 4) {
                         const float4 a = ks[e / 4], b = kl[e / 4];
                         const float2 x = __ffma2_rn(make_float2(v[e], v[e + 1]), make_float2(a.x, a.y),
-                                                    __fmul2_rn(make_float2(b.x, b.y), qs2));
+                                                    __ffma2_rn(make_float2(b.x, b.y), qs2, nm2));
                         const float2 y =
                             __ffma2_rn(make_float2(v[e + 2], v[e + 3]), make_float2(a.z, a.w),
-                                       __fmul2_rn(make_float2(b.z, b.w), qs2));
+                                       __ffma2_rn(make_float2(b.z, b.w), qs2, nm2));
                         v[e] = x.x;
                         v[e + 1] = x.y;
                         v[e + 2] = y.x;
@@ -423,89 +444,92 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
                     }
                     if (!interior) {
 #pragma unroll
-                        for (int e = 0; e < W; ++e)
+                        for (int e = 0; e < 32; ++e)
                             if (p0 + cb + e > limit) v[e] = -INFINITY;
                     }
-                };
-                float mx = -INFINITY;
+                    float mx = -INFINITY;
 #pragma unroll
-                for (int ch = 0; ch < kChunks; ++ch) {
-                    scores(c0 + ch * W);
+                    for (int e = 0; e < 32; e += 2) mx = max3(mx, v[e], v[e + 1]);
+                    // (before a row's first visible position its maximum is -inf and nm is 0)
+                    const bool grow = mx > (m == -INFINITY ? -INFINITY : kRescaleLog2);
+                    if (__any_sync(FULL, grow)) {
+                        const float f = grow && m != -INFINITY ? ex2(-mx) : 1.f;
+                        if (lt > seg_lo) {
+                            // O holds the share's earlier tiles: wait for the P V of tile t - 1.
+                            // (Its barrier is in phase t - 3 or t - 1: S of tile t - 1 waited for
+                            // the former, and tile t + 1's P V needs this warp's arrival.)
+                            const bool done = mbar_wait(BAR(PD + ((t - 1) & 1)), ((t - 1) >> 1) & 1,
+                                                        abort_flag, p.dev_err, p.wait_ns);
+                            if (!__all_sync(FULL, done)) {
+                                ok_run = false;
+                                break;
+                            }
+                            tc_after();
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t o[16];
+                                tmem_ld16(lane_base + kColO + c * 16, o);
 #pragma unroll
-                    for (int e = 0; e < W; e += 2) mx = max3(mx, v[e], v[e + 1]);
-                }
-                const bool grow = mx > m + kRescaleLog2;
-                const bool rescale = grow && m != -INFINITY;
-                if (__any_sync(FULL, rescale)) {
-                    // O holds the share's tiles before t: wait for the P V of tile t - 1.  (Its
-                    // barrier is in phase t - 3 or t - 1: S of tile t - 1 waited for the former,
-                    // and tile t + 1's P V needs this warp's arrival.)
-                    const bool done = mbar_wait(BAR(PD + ((t - 1) & 1)), ((t - 1) >> 1) & 1,
-                                                abort_flag, p.dev_err, p.wait_ns);
-                    if (!__all_sync(FULL, done)) {
-                        ok_run = false;
-                        break;
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st16(lane_base + kColO + c * 16, o);
+                            }
+                        }
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+#pragma unroll 1
+                        for (int c = 0; c < ch; ++c) {  // this tile's weights so far
+                            uint32_t w[16];
+                            tmem_ld16(s_addr + c0 / 2 + c * 16, w);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                w[e] = pack_bf16(bf16_lo(w[e]) * f, bf16_hi(w[e]) * f);
+                            tmem_st16(s_addr + c0 / 2 + c * 16, w);
+                        }
+                        l2.x *= f;
+                        l2.y *= f;
+                        cr2.x *= f;
+                        cr2.y *= f;
+                        if (grow) {
+                            m = mx - nm;
+                            nm = -m;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] -= mx;
+                        }
                     }
-                    tc_after();
-                    const float f = rescale ? ex2(m - mx) : 1.f;
-                    float o[32];
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        tmem_ld32(lane_base + kColO + c * 32, o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= f;
-                        tmem_st32(lane_base + kColO + c * 32, o);
-                    }
-                    l2.x *= f;
-                    l2.y *= f;
-                    cr2.x *= f;
-                    cr2.y *= f;
-                }
-                if (grow) m = mx;
-                const float nm = m == -INFINITY ? 0.f : -m;
-                const float2 nm2 = make_float2(nm, nm);
-                uint32_t pk[NC / 2];
-#pragma unroll
-                for (int ch = 0; ch < kChunks; ++ch) {
-                    const int cb = c0 + ch * W;
-                    if (kChunks > 1) scores(cb);
                     const float4 *vs = reinterpret_cast<const float4 *>(par + 2 * kTile + cb);
                     const float4 *vl = reinterpret_cast<const float4 *>(par + 3 * kTile + cb);
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < W; e += 4) {
+                    for (int e = 0; e < 32; e += 4) {
                         const float4 a = vs[e / 4], b = vl[e / 4];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float2 x = make_float2(v[e + 2 * h], v[e + 2 * h + 1]);
+                        for (int h = 0; h < 4; h += 2) {
                             float2 s2 = h ? make_float2(a.z, a.w) : make_float2(a.x, a.y);
                             float2 b2 = h ? make_float2(b.z, b.w) : make_float2(b.x, b.y);
                             if (!interior) {  // a hidden position's NaN must not get through
-                                if (x.x == -INFINITY) s2.x = b2.x = 0.f;
-                                if (x.y == -INFINITY) s2.y = b2.y = 0.f;
+                                if (v[e + h] == -INFINITY) s2.x = b2.x = 0.f;
+                                if (v[e + h + 1] == -INFINITY) s2.y = b2.y = 0.f;
                             }
-                            const float2 d = __fadd2_rn(x, nm2);
-                            const float2 pe = make_float2(ex2(d.x), ex2(d.y));
+                            const float2 pe = make_float2(ex2(v[e + h]), ex2(v[e + h + 1]));
                             l2 = __fadd2_rn(l2, pe);
                             cr2 = __ffma2_rn(pe, b2, cr2);
                             const float2 w = __fmul2_rn(pe, s2);
-                            pk[(ch * W + e) / 2 + h] = pack_bf16(w.x, w.y);
+                            pk[(e + h) / 2] = pack_bf16(w.x, w.y);
                         }
                     }
+                    // P over the columns of S that this warp has read
+                    tmem_st16(s_addr + cb / 2, pk);
                 }
-                // P over S: this copy's columns at c0 / 2, zeros in the other copies'
-                if constexpr (NCP == 1) {
-                    tmem_st64(s_addr, pk);
-                } else {
-                    uint32_t prow[kTile / 2];
+                if (!ok_run) break;
+                if constexpr (NCP > 1) {  // zeros in the other copies' columns
+                    uint32_t z[16];
 #pragma unroll
-                    for (int i = 0; i < kTile / 2; ++i) prow[i] = 0u;
-#pragma unroll
-                    for (int q = 0; q < NCP; ++q)
-                        if (q == cp)
-#pragma unroll
-                            for (int i = 0; i < NC / 2; ++i) prow[q * (NC / 2) + i] = pk[i];
-                    tmem_st64(s_addr, prow);
+                    for (int e = 0; e < 16; ++e) z[e] = 0u;
+#pragma unroll 1
+                    for (int c = 0; c < kTile / 2; c += 16)
+                        if (c / (NC / 2) != cp) tmem_st16(s_addr + c, z);
                 }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_before();
                 mbar_arrive(BAR(PF + s));
             }

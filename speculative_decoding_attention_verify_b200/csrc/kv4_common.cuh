@@ -102,21 +102,31 @@ __device__ __forceinline__ float *kv4_slot_ml(const Kv4Params &p, int64_t slot, 
     return p.ws + (int64_t)p.n_slots * rows * p.head_dim + (slot * rows + lr) * 2;
 }
 
+// Sequence b or the next one with work (batch at the end).  Out of line: cursors move to another
+// sequence rarely, and the tile loops have to stay small.
+static __device__ __noinline__ int kv4_next_sequence(const Kv4Params &p, int b) {
+    for (; b < p.batch; ++b) {
+        int q0, n_q, kv_len;
+        bool bad;
+        if (kv4_sequence(p, b, q0, n_q, kv_len, bad)) break;
+    }
+    return b;
+}
+
 // A position in the list of tiles: tile t of unit (b, g), with the sequence's row data.
 struct Kv4Cursor {
     int b, g, t, tiles;
     int q0, n_q, kv_len;
     // Sequence b or the next one with work (b = batch at the end).
     __device__ __forceinline__ void load(const Kv4Params &p) {
-        for (; b < p.batch; ++b) {
-            bool bad;
-            if (kv4_sequence(p, b, q0, n_q, kv_len, bad)) {
-                tiles = (kv_len + kKv4Tile - 1) / kKv4Tile;
-                return;
-            }
-        }
+        b = kv4_next_sequence(p, b);
         tiles = 1;
         kv_len = 0;
+        if (b >= p.batch) return;
+        q0 = __ldg(p.q_start + b);
+        n_q = __ldg(p.q_start + b + 1) - q0;
+        kv_len = __ldg(p.kv_len + b);
+        tiles = (kv_len + kKv4Tile - 1) / kKv4Tile;
     }
     // n tiles on, within the unit or to the start of the next one.
     __device__ __forceinline__ void skip(const Kv4Params &p, int n) {

@@ -104,7 +104,7 @@ __device__ __forceinline__ int m_of(int r) { return (r & 8) | ((r & 3) << 1) | (
 __device__ __forceinline__ int pos_of(int m) { return (m & 8) | ((m & 1) << 2) | ((m >> 1) & 3); }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_mma_kernel(const Kv4Params p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
     pdl_trigger();  // (see launch_pdl)
     pdl_wait();
     using C = MmaCfg<D, NT>;

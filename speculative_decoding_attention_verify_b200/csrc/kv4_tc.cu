@@ -31,6 +31,8 @@
 // 16 KB of codes become 64 KB written and read again by the tensor core.
 // Every wait on an mbarrier is bounded (see sd_set_wait_timeout_ns); on expiry the CTA records
 // SD_DEVERR_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
+#include <type_traits>
+
 #include "kv4_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -94,7 +96,7 @@ __device__ __forceinline__ void copy4z(uint32_t dst, const void *src, bool in) {
                  : "memory");
 }
 
-// 16 consecutive columns of this thread's TMEM lane.  The store is not waited for: a wait::st comes
+// 16 consecutive columns of this thread's TMEM lane.  Stores are not waited for: a wait::st comes
 // before the columns are loaded again or handed to the tensor core.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -117,11 +119,66 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
+// 32 columns of 32 lanes in the accumulator layout of an m16n8 fragment: lane (g, t) of the warp
+// gets rows g + 8 k (k = 0..3), columns 8 i + 2 t and 8 i + 2 t + 1 (i = 0..3) in
+// v[k / 2][4 i + 2 (k % 2)] and the element after it.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[2][16]) {
+    uint32_t r[2][16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3]), "=r"(r[h][4]),
+              "=r"(r[h][5]), "=r"(r[h][6]), "=r"(r[h][7]), "=r"(r[h][8]), "=r"(r[h][9]),
+              "=r"(r[h][10]), "=r"(r[h][11]), "=r"(r[h][12]), "=r"(r[h][13]), "=r"(r[h][14]),
+              "=r"(r[h][15])
+            : "r"(taddr + ((uint32_t)h << 20))
+            : "memory");
+    // (the values pass through the wait, so no use can move before it)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0][0]), "+r"(r[0][1]), "+r"(r[0][2]), "+r"(r[0][3]), "+r"(r[0][4]),
+                   "+r"(r[0][5]), "+r"(r[0][6]), "+r"(r[0][7]), "+r"(r[0][8]), "+r"(r[0][9]),
+                   "+r"(r[0][10]), "+r"(r[0][11]), "+r"(r[0][12]), "+r"(r[0][13]), "+r"(r[0][14])
+                 :
+                 : "memory");
+    asm volatile(""
+                 : "+r"(r[0][15]), "+r"(r[1][0]), "+r"(r[1][1]), "+r"(r[1][2]), "+r"(r[1][3]),
+                   "+r"(r[1][4]), "+r"(r[1][5]), "+r"(r[1][6]), "+r"(r[1][7]), "+r"(r[1][8]),
+                   "+r"(r[1][9]), "+r"(r[1][10]), "+r"(r[1][11]), "+r"(r[1][12]), "+r"(r[1][13]),
+                   "+r"(r[1][14]), "+r"(r[1][15])
+                 :
+                 : "memory");
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[h][e] = __uint_as_float(r[h][e]);
+}
+
+// The same layout's pairs of columns, packed to bf16: 16 columns of 32 lanes (lane (g, t): rows
+// g + 8 k, column 4 i + t in w[k / 2][2 i + k % 2]).
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&w)[2][8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile(
+            "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                taddr + ((uint32_t)h << 20)),
+            "r"(w[h][0]), "r"(w[h][1]), "r"(w[h][2]), "r"(w[h][3]), "r"(w[h][4]), "r"(w[h][5]),
+            "r"(w[h][6]), "r"(w[h][7])
+            : "memory");
+}
+
+// The bounded wait's slow part, out of the hot code.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                       int32_t *dev_err, unsigned long long limit_ns) {
+    return mbar_wait(bar, parity, abort_flag, dev_err, limit_ns);
+}
+
 // Column of channel e (0..7) within its group of 8, and the channel order of a group's columns.
 __device__ __forceinline__ constexpr int col_of(int e) { return e < 4 ? 2 * e : 2 * (e - 4) + 1; }
 
 template <int D, int NCP>
-__global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) {
+__global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_constant__ Kv4Params p) {
     pdl_trigger();  // (see launch_pdl)
     pdl_wait();
     using C = TcCfg<D>;
@@ -178,10 +235,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
     __syncthreads();
     tc_after();
     const uint32_t tmem = s_tmem;
+    auto wait = [&](int bar, int parity) {
+        return mbar_try(BAR(bar), parity & 1) ||
+               wait_slow(BAR(bar), parity & 1, abort_flag, p.dev_err, p.wait_ns);
+    };
     // One lane waits; the outcome is the warp's.
     auto wait1 = [&](int bar, int parity) {
         bool ok = true;
-        if (lane == 0) ok = mbar_wait(BAR(bar), parity & 1, abort_flag, p.dev_err, p.wait_ns);
+        if (lane == 0) ok = wait(bar, parity);
         return __shfl_sync(FULL, ok ? 1 : 0, 0) != 0;
     };
 
@@ -270,12 +331,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
                 const uint32_t *par = reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes);
                 // (lanes 0-15 the key's two, lanes 16-31 the value's)
                 const uint32_t w = par[lane];
+                // per pair of positions: two scales, two offsets
                 float *d = s_par + (t % kParSlots) * 4 * kTile + (lane >> 4) * 2 * kTile +
-                           ew * kPageSize + (lane & 15);
+                           (ew * (kPageSize / 2) + ((lane & 15) >> 1)) * 4 + (lane & 1);
                 const float sc = param_scale(w), lw = param_low(w);
                 const float a = lane < 16 ? sc * p.scale_log2 : sc;
                 d[0] = a;
-                d[kTile] = lane < 16 ? fmaf(lw, p.scale_log2, -16.f * a) : fmaf(8.f, a, lw);
+                d[2] = lane < 16 ? fmaf(lw, p.scale_log2, -16.f * a) : fmaf(8.f, a, lw);
             }
             expand(st, sK + s * C::kTileBytes, [](uint32_t x) { return x; });
             if (lane == 0) mbar_arrive(BAR(KF + s));
@@ -394,75 +456,123 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
         float qsum = write_q(u);
         bool ok_run = true;
         int t = 0, seg = 0;
+        // The softmax itself works on fragments: lane (g, t4) has rows g + 8 k (k = 0..3) of the
+        // warp's 32 and two of every eight columns, so a position's factors are loaded by a
+        // quarter of the lanes and used for four rows each.
+        const int gq = lane >> 2, t4 = lane & 3;
         while (t < n_my) {
             const int n_seg = min(u.tiles - u.t, n_my - t);
             const bool starts = u.t == 0, ends = u.t + n_seg == u.tiles;
             const int R = u.n_q * G;
             const bool row_ok = r < R;
-            const int limit = row_ok ? u.kv_len - u.n_q + r / G : -1;
             const int first_limit = u.kv_len - u.n_q;
-            float m = -INFINITY, nm = 0.f;
             const int seg_lo = u.t;
-            float2 l2 = make_float2(0.f, 0.f), cr2 = make_float2(0.f, 0.f);
-            const float2 qs2 = make_float2(qsum, qsum);
+            float mk[4], nm[4], qs[4];
+            int limit[4];  // last visible position (rows past R see nothing)
+            float2 l2[4], cr2[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int rk = warp * 32 + gq + 8 * k - cp * RPC;
+                mk[k] = -INFINITY;
+                nm[k] = 0.f;
+                qs[k] = __shfl_sync(FULL, qsum, gq + 8 * k);
+                limit[k] = rk < R ? first_limit + rk / G : -1;
+                l2[k] = cr2[k] = make_float2(0.f, 0.f);
+            }
+            // value of row `lane` from the lanes that hold it
+            auto by_row = [&](const float (&x)[4]) {
+                float y = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float z = __shfl_sync(FULL, x[k], (lane & 7) * 4);
+                    if ((lane >> 3) == k) y = z;
+                }
+                return y;
+            };
             const int t_end = t + n_seg;
             for (int lt = u.t; ok_run && t < t_end; ++t, ++lt) {
                 const int s = t & 1;
-                const bool got =
-                    mbar_wait(BAR(SF + s), (t >> 1) & 1, abort_flag, p.dev_err, p.wait_ns);
-                if (!__all_sync(FULL, got)) {
+                if (!__all_sync(FULL, wait(SF + s, t >> 1))) {
                     ok_run = false;
                     break;
                 }
                 tc_after();
                 const uint32_t s_addr = lane_base + s * kTile;
-                const float *par = s_par + (t % kParSlots) * 4 * kTile;
+                const float4 *par =
+                    reinterpret_cast<const float4 *>(s_par + (t % kParSlots) * 4 * kTile) + t4;
                 const int p0 = lt * kTile;
                 // every row sees every position of the tile (rows past R may compute anything)
                 const bool interior = p0 + kTile - 1 <= first_limit;
-#pragma unroll 1
-                for (int ch = 0; ch < NC / 32; ++ch) {
+                // 32 columns (instantiated apart for tiles that need no mask); false: a wait failed
+                auto chunk = [&](int ch, auto masked) {
+                    constexpr bool kMasked = decltype(masked)::value;
                     const int cb = c0 + ch * 32;
-                    float v[32];
-                    tmem_ld32(s_addr + cb, v);
+                    float v[2][16];
+                    tmem_ld_frag(s_addr + cb, v);
                     // exponents of the weights: the scores in log2 units less the maximum
-                    const float4 *ks = reinterpret_cast<const float4 *>(par + cb);
-                    const float4 *kl = reinterpret_cast<const float4 *>(par + kTile + cb);
-                    const float2 nm2 = make_float2(nm, nm);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 a = ks[e / 4], b = kl[e / 4];
-                        const float2 x = __ffma2_rn(make_float2(v[e], v[e + 1]), make_float2(a.x, a.y),
-                                                    __ffma2_rn(make_float2(b.x, b.y), qs2, nm2));
-                        const float2 y =
-                            __ffma2_rn(make_float2(v[e + 2], v[e + 3]), make_float2(a.z, a.w),
-                                       __ffma2_rn(make_float2(b.z, b.w), qs2, nm2));
-                        v[e] = x.x;
-                        v[e + 1] = x.y;
-                        v[e + 2] = y.x;
-                        v[e + 3] = y.y;
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 f = par[cb / 2 + 4 * i];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float &a = v[k >> 1][4 * i + 2 * (k & 1)];
+                            float &b = v[k >> 1][4 * i + 2 * (k & 1) + 1];
+                            const float2 x = __ffma2_rn(
+                                make_float2(a, b), make_float2(f.x, f.y),
+                                __ffma2_rn(make_float2(f.z, f.w), make_float2(qs[k], qs[k]),
+                                           make_float2(nm[k], nm[k])));
+                            a = x.x;
+                            b = x.y;
+                        }
                     }
-                    if (!interior) {
+                    if constexpr (kMasked) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (p0 + cb + e > limit) v[e] = -INFINITY;
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    if (p0 + cb + 8 * i + 2 * t4 + c > limit[k])
+                                        v[k >> 1][4 * i + 2 * (k & 1) + c] = -INFINITY;
                     }
-                    float mx = -INFINITY;
+                    float mx[4];
+                    bool grow = false;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) mx = max3(mx, v[e], v[e + 1]);
-                    // (before a row's first visible position its maximum is -inf and nm is 0)
-                    const bool grow = mx > (m == -INFINITY ? -INFINITY : kRescaleLog2);
+                    for (int k = 0; k < 4; ++k) {
+                        const float *x = &v[k >> 1][2 * (k & 1)];
+                        mx[k] = max3(max3(x[0], x[1], x[4]), max3(x[5], x[8], x[9]),
+                                     fmaxf(x[12], x[13]));
+                        // (before a row's first visible position its maximum is -inf and nm is 0)
+                        grow |= mx[k] > (mk[k] == -INFINITY ? -INFINITY : kRescaleLog2);
+                    }
                     if (__any_sync(FULL, grow)) {
-                        const float f = grow && m != -INFINITY ? ex2(-mx) : 1.f;
+                        float f[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float x = fmaxf(mx[k], __shfl_xor_sync(FULL, mx[k], 1));
+                            x = fmaxf(x, __shfl_xor_sync(FULL, x, 2));
+                            const bool up = x > (mk[k] == -INFINITY ? -INFINITY : kRescaleLog2);
+                            f[k] = up && mk[k] != -INFINITY ? ex2(-x) : 1.f;
+                            if (up) {
+                                mk[k] = x - nm[k];
+                                nm[k] = -mk[k];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                    for (int c = 0; c < 2; ++c) v[k >> 1][4 * i + 2 * (k & 1) + c] -= x;
+                            }
+                            l2[k].x *= f[k];
+                            l2[k].y *= f[k];
+                            cr2[k].x *= f[k];
+                            cr2[k].y *= f[k];
+                        }
+                        const float fr = by_row(f);
                         if (lt > seg_lo) {
                             // O holds the share's earlier tiles: wait for the P V of tile t - 1.
                             // (Its barrier is in phase t - 3 or t - 1: S of tile t - 1 waited for
                             // the former, and tile t + 1's P V needs this warp's arrival.)
-                            const bool done = mbar_wait(BAR(PD + ((t - 1) & 1)), ((t - 1) >> 1) & 1,
-                                                        abort_flag, p.dev_err, p.wait_ns);
-                            if (!__all_sync(FULL, done)) {
-                                ok_run = false;
-                                break;
+                            if (!__all_sync(FULL, wait(PD + ((t - 1) & 1), (t - 1) >> 1))) {
+                                return false;
                             }
                             tc_after();
 #pragma unroll 1
@@ -471,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
                                 tmem_ld16(lane_base + kColO + c * 16, o);
 #pragma unroll
                                 for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * fr);
                                 tmem_st16(lane_base + kColO + c * 16, o);
                             }
                         }
@@ -482,43 +592,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
                             tmem_ld16(s_addr + c0 / 2 + c * 16, w);
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                w[e] = pack_bf16(bf16_lo(w[e]) * f, bf16_hi(w[e]) * f);
+                                w[e] = pack_bf16(bf16_lo(w[e]) * fr, bf16_hi(w[e]) * fr);
                             tmem_st16(s_addr + c0 / 2 + c * 16, w);
                         }
-                        l2.x *= f;
-                        l2.y *= f;
-                        cr2.x *= f;
-                        cr2.y *= f;
-                        if (grow) {
-                            m = mx - nm;
-                            nm = -m;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] -= mx;
-                        }
                     }
-                    const float4 *vs = reinterpret_cast<const float4 *>(par + 2 * kTile + cb);
-                    const float4 *vl = reinterpret_cast<const float4 *>(par + 3 * kTile + cb);
-                    uint32_t pk[16];
+                    uint32_t pk[2][8];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 a = vs[e / 4], b = vl[e / 4];
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 f = par[kTile / 2 + cb / 2 + 4 * i];
 #pragma unroll
-                        for (int h = 0; h < 4; h += 2) {
-                            float2 s2 = h ? make_float2(a.z, a.w) : make_float2(a.x, a.y);
-                            float2 b2 = h ? make_float2(b.z, b.w) : make_float2(b.x, b.y);
-                            if (!interior) {  // a hidden position's NaN must not get through
-                                if (v[e + h] == -INFINITY) s2.x = b2.x = 0.f;
-                                if (v[e + h + 1] == -INFINITY) s2.y = b2.y = 0.f;
+                        for (int k = 0; k < 4; ++k) {
+                            const float a = v[k >> 1][4 * i + 2 * (k & 1)];
+                            const float b = v[k >> 1][4 * i + 2 * (k & 1) + 1];
+                            float2 sc = make_float2(f.x, f.y), lw = make_float2(f.z, f.w);
+                            if constexpr (kMasked) {  // a hidden position's NaN must not get through
+                                if (a == -INFINITY) sc.x = lw.x = 0.f;
+                                if (b == -INFINITY) sc.y = lw.y = 0.f;
                             }
-                            const float2 pe = make_float2(ex2(v[e + h]), ex2(v[e + h + 1]));
-                            l2 = __fadd2_rn(l2, pe);
-                            cr2 = __ffma2_rn(pe, b2, cr2);
-                            const float2 w = __fmul2_rn(pe, s2);
-                            pk[(e + h) / 2] = pack_bf16(w.x, w.y);
+                            const float2 pe = make_float2(ex2(a), ex2(b));
+                            l2[k] = __fadd2_rn(l2[k], pe);
+                            cr2[k] = __ffma2_rn(pe, lw, cr2[k]);
+                            const float2 w = __fmul2_rn(pe, sc);
+                            pk[k >> 1][2 * i + (k & 1)] = pack_bf16(w.x, w.y);
                         }
                     }
                     // P over the columns of S that this warp has read
-                    tmem_st16(s_addr + cb / 2, pk);
+                    tmem_st_frag(s_addr + cb / 2, pk);
+                    return true;
+                };
+                if (interior) {
+#pragma unroll 1
+                    for (int ch = 0; ok_run && ch < NC / 32; ++ch)
+                        ok_run = chunk(ch, std::false_type{});
+                } else {
+#pragma unroll 1
+                    for (int ch = 0; ok_run && ch < NC / 32; ++ch)
+                        ok_run = chunk(ch, std::true_type{});
                 }
                 if (!ok_run) break;
                 if constexpr (NCP > 1) {  // zeros in the other copies' columns
@@ -539,12 +648,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Params p) 
             nx.skip(p, n_seg);
             if (ok_run && t < n_my) qsum = write_q(nx);
             bool done = ok_run;
-            if (ok_run) done = mbar_wait(BAR(SD), seg & 1, abort_flag, p.dev_err, p.wait_ns);
+            if (ok_run) done = wait(SD, seg);
             ++seg;
             const bool read_o = __all_sync(FULL, done);
             if (!read_o) ok_run = false;
             tc_after();
-            float l = l2.x + l2.y, cr = cr2.x + cr2.y;
+            // from here on a lane is one row again
+            float lk[4], ck[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                lk[k] = l2[k].x + l2[k].y;
+                ck[k] = cr2[k].x + cr2[k].y;
+#pragma unroll
+                for (int x = 1; x < 4; x <<= 1) {
+                    lk[k] += __shfl_xor_sync(FULL, lk[k], x);
+                    ck[k] += __shfl_xor_sync(FULL, ck[k], x);
+                }
+            }
+            float m = by_row(mk), l = by_row(lk);
+            const float cr = by_row(ck);
             if (l != l && m == -INFINITY) m = 0.f;  // (a NaN sum survives the merges)
             float fq[NCP];
             if constexpr (NCP > 1) {

@@ -168,10 +168,22 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&w)
             : "memory");
 }
 
-// The bounded wait's slow part, out of the hot code.
+// Bounded wait, out of the hot code: plain polls (the hardware suspends each for a while and wakes
+// it when the phase completes; a poll with a time of its own sleeps in steps, and the kernel's
+// roles hand over to one another several times per tile), the clock and the abort flag every 64.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                        int32_t *dev_err, unsigned long long limit_ns) {
-    return mbar_wait(bar, parity, abort_flag, dev_err, limit_ns);
+    const unsigned long long t0 = now_ns();
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (now_ns() - t0 > limit_ns) {
+            *abort_flag = 1;
+            set_dev_err(dev_err, SD_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
 }
 
 // Column of channel e (0..7) within its group of 8, and the channel order of a group's columns.
@@ -186,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
     constexpr int RPC = kRows / NCP;          // rows per copy
     constexpr int NC = kTile / NCP;           // columns of a softmax warp
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // (an offset from the array, so that accesses stay shared-memory instructions)
+    uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
     __shared__ long long s_red[2 * kThreads / 32];
     __shared__ Kv4Start s_start;
     __shared__ uint32_t s_tmem;
@@ -299,20 +311,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
         for (int i = 0; i < kStages - 1; ++i) copy_next();
         // lane: row (lane & 15), chunks (lane >> 4), (lane >> 4) + 2
         auto expand = [&](const uint8_t *src, uint8_t *dst, auto &&f) {
-            const int r = lane & 15, row = ew * kPageSize + r;
+            const int r = lane & 15;
+            // word c of chunk q is 16-byte chunk 4 (q & 1) + c of the row in half q / 2
+            const uint32_t at = (uint32_t)((ew * kPageSize + r) * 128) |
+                                (uint32_t)((((lane >> 4) * 4) ^ (r & 7)) << 4);
 #pragma unroll
             for (int k = 0; k < Q / 2; ++k) {
-                const int q = 2 * k + (lane >> 4);
-                const uint4 x = *reinterpret_cast<const uint4 *>(src + raw_at(r, q));
+                const uint4 x = *reinterpret_cast<const uint4 *>(src + raw_at(r, 2 * k + (lane >> 4)));
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int slot = 4 * q + c;  // 8 channels: 16-byte chunk of the bf16 row
-                    *reinterpret_cast<uint4 *>(dst + (slot >> 3) * kHalfBytes + row * 128 +
-                                               (((slot & 7) ^ (row & 7)) << 4)) =
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint4 *>(dst + k * kHalfBytes + (at ^ (uint32_t)(c << 4))) =
                         make_uint4(f(pair_at(w[c], 0)), f(pair_at(w[c], 1)), f(pair_at(w[c], 2)),
                                    f(pair_at(w[c], 3)));
-                }
             }
             fence_async_smem();
             __syncwarp();
@@ -354,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
         int seg = 0;
         for (int t = 0; t < n_my; ++t) {
             const int s = t & 1;
+            // (what comes last is waited for last)
             bool ok = true;
             if (t == 0 || c.t == 0) ok = wait1(QF, seg++);  // a unit's share begins
             ok = ok && wait1(KF + s, t >> 1) && (t < 2 || wait1(PD + s, (t - 2) >> 1));
@@ -389,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
         Kv4Cursor c = first;
         for (int t = 0; t < n_my; ++t) {
             const int s = t & 1;
-            if (!(wait1(PF + s, t >> 1) && wait1(VF + s, t >> 1))) break;
+            if (!(wait1(VF + s, t >> 1) && wait1(PF + s, t >> 1))) break;
             tc_after();
             const bool fresh = t == 0 || c.t == 0;
             const bool last = t + 1 == n_my || c.t + 1 == c.tiles;

@@ -71,8 +71,12 @@ sd_status make_rope(const sd_rope_desc *r, int head_dim, RopeParams *out) {
         if (!(hi > lo)) hi = lo + 0.001;
         if (!(r->gain > 0.f)) out->gain = 0.1 * log(factor) + 1.0;
     }
-    for (int m = 0; m < n / 2; ++m) {
-        double f = pow(theta, -2.0 * m / n);
+    // theta^(-2m/n) as powers of one root, in long double: 64 products are off by less than an
+    // eighth of a double's last place, and cost less than one pow
+    const long double root = powl((long double)theta, -2.0L / n);
+    long double power = 1.0L;
+    for (int m = 0; m < n / 2; ++m, power *= root) {
+        double f = (double)power;
         if (r->scaling == SD_ROPE_LINEAR) f /= factor;
         if (r->scaling == SD_ROPE_YARN) {
             const double t = fmin(1.0, fmax(0.0, (m - lo) / (hi - lo)));

@@ -130,19 +130,29 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle and the current device without building torch objects for them (a
+# torch.cuda.Stream costs 3.5 us, as much as a launch); the public calls where torch has neither.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return ctypes.c_void_p(_raw_stream(_raw_device()))
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _on(t: torch.Tensor):
     """Make the tensor's device current for the call (the library launches on the current
     device, and sd_verify_attention_noalloc picks its per-device scratch from it)."""
-    if t.device.type == "cuda" and t.device.index is not None and \
-            t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return contextlib.nullcontext()
+    device = t.device
+    if device.type == "cuda" and device.index is not None and device.index != _raw_device():
+        return torch.cuda.device(device)
+    return _HERE
 
 
 def _check(status: int, where: str):
@@ -187,7 +197,9 @@ class KVCache:
             d.max_pages_per_seq = block_table.shape[1]
             d.num_pages = k.shape[0]
         d.kv_len = _ptr(kv_len)
-        self.desc = d
+        self.desc, self.ref = d, ctypes.byref(d)
+        self.row_shape = (d.dtype, d.h_kv, d.head_dim, kv_len.shape[0], k.device)
+        self.room = k.shape[2] if block_table is None else None
 
     @property
     def batch(self) -> int:
@@ -214,7 +226,7 @@ class Queries:
         d.max_kv_len = int(max_kv_len)
         d.softmax_scale = float(softmax_scale)
         d.q_start = _ptr(q_start)
-        self.desc = d
+        self.desc, self.ref = d, ctypes.byref(d)
 
     @property
     def rows(self) -> int:
@@ -549,7 +561,7 @@ class Rope:
                 raise ValueError("Rope: inv_freq holds rotary_dim / 2 frequencies")
             self._table = (ctypes.c_float * len(table))(*table)
             d.inv_freq = ctypes.cast(self._table, ctypes.c_void_p)
-        self.desc = d
+        self.desc, self.ref = d, ctypes.byref(d)
 
 
 def _row_tensor(t: torch.Tensor, rows: int, what: str) -> int:
@@ -584,8 +596,9 @@ class NewRows:
             if t is not None and t.device != k.device:
                 raise ValueError("NewRows: tensors must live on one device")
         self.q, self.k, self.v, self.q_start, self.pos = q, k, v, q_start, pos
-        self.dtype = _dtype_code(k)
-        self.batch = q_start.shape[0] - 1
+        self.batch, self.max_kv_len = q_start.shape[0] - 1, int(max_kv_len)
+        # what the cache's row_shape has to be
+        self.shape = (_dtype_code(k), k.shape[1], k.shape[2], self.batch, k.device)
         d = sd_rows_desc()
         d.n_rows, d.max_kv_len = n, int(max_kv_len)
         d.k, d.v = k.data_ptr(), v.data_ptr()
@@ -593,7 +606,7 @@ class NewRows:
         d.q_start, d.pos = _ptr(q_start), _ptr(pos)
         if q is not None:
             d.h_q, d.q, d.q_stride = q.shape[1], q.data_ptr(), _row_tensor(q, n, "q")
-        self.desc = d
+        self.desc, self.ref = d, ctypes.byref(d)
 
 
 class KV4Cache:
@@ -642,7 +655,9 @@ class KV4Cache:
             d.max_pages_per_seq = block_table.shape[1]
             d.num_pages = k.shape[0]
         d.kv_len = _ptr(kv_len)
-        self.desc = d
+        self.desc, self.ref = d, ctypes.byref(d)
+        self.row_shape = (d.dtype, d.h_kv, d.head_dim, kv_len.shape[0], k.device)
+        self.room = k.shape[2] if block_table is None else None
 
     @classmethod
     def empty(cls, batch: int, h_kv: int, l_cap: int, head_dim: int, kv_len: torch.Tensor,
@@ -667,12 +682,10 @@ class KV4Cache:
 
 
 def _check_rows(rows: NewRows, cache, where: str):
-    d, c = rows.desc, cache.desc
-    if rows.dtype != c.dtype or rows.k.shape[1] != c.h_kv or rows.k.shape[2] != c.head_dim:
-        raise ValueError(f"{where}: the rows' dtype, KV heads and head_dim must be the cache's")
-    if rows.batch != cache.batch or rows.k.device != cache.k.device:
-        raise ValueError(f"{where}: rows and cache must hold one batch on one device")
-    if c.page_size == 0 and d.max_kv_len > cache.k.shape[2]:
+    if rows.shape != cache.row_shape:
+        raise ValueError(f"{where}: the rows' dtype, KV heads and head_dim must be the cache's, and "
+                         "both must hold one batch on one device")
+    if cache.room is not None and rows.max_kv_len > cache.room:
         raise ValueError(f"{where}: max_kv_len exceeds the cache's room")
 
 
@@ -696,9 +709,9 @@ def sd_kv_append(rope: Optional[Rope], rows: NewRows, cache: KVCache, q_out=None
     _check_rows(rows, cache, "sd_kv_append")
     q_out = _rows_out(q_out, rows.q, "sd_kv_append")
     with _on(rows.k):
-        _check(lib().sd_kv_append(ctypes.byref(rope.desc) if rope is not None else None,
-                                  ctypes.byref(rows.desc), ctypes.byref(cache.desc), cache.batch,
-                                  _ptr(q_out), _ptr(dev_err), _stream(stream)), "sd_kv_append")
+        _check(lib().sd_kv_append(rope.ref if rope is not None else None, rows.ref, cache.ref,
+                                  rows.batch, _ptr(q_out), _ptr(dev_err), _stream(stream)),
+               "sd_kv_append")
     return q_out
 
 
@@ -712,10 +725,9 @@ def sd_kv4_append(rope: Optional[Rope], rows: NewRows, cache: KV4Cache, q_out=No
         if t is not None:
             _rows_out(t, rows.k, "sd_kv4_append")
     with _on(rows.k):
-        _check(lib().sd_kv4_append(ctypes.byref(rope.desc) if rope is not None else None,
-                                   ctypes.byref(rows.desc), ctypes.byref(cache.desc), cache.batch,
-                                   _ptr(q_out), _ptr(k_out), _ptr(v_out), _ptr(dev_err),
-                                   _stream(stream)), "sd_kv4_append")
+        _check(lib().sd_kv4_append(rope.ref if rope is not None else None, rows.ref, cache.ref,
+                                   rows.batch, _ptr(q_out), _ptr(k_out), _ptr(v_out),
+                                   _ptr(dev_err), _stream(stream)), "sd_kv4_append")
     return q_out
 
 
@@ -730,16 +742,17 @@ def sd_kv4_attention_workspace_size(q: Queries, kv: KV4Cache) -> int:
 def sd_kv4_verify_attention(q: Queries, kv: KV4Cache, out=None, workspace=None, dev_err=None,
                             stream=None) -> torch.Tensor:
     """Dense attention of the queries over a 4-bit cache (sd_verify_attention's mask)."""
-    if q.q.dtype != kv.dtype or q.q.shape[2] != kv.head_dim or q.q_start.shape[0] != kv.batch + 1:
-        raise ValueError("sd_kv4_verify_attention: queries and cache differ in dtype, head_dim or "
-                         "batch")
-    if kv.block_table is None and q.desc.max_kv_len > kv.k.shape[2]:
+    t = q.q
+    if t.dtype != kv.dtype or t.shape[2] != kv.row_shape[2] or \
+            q.q_start.shape[0] != kv.row_shape[3] + 1 or t.device != kv.row_shape[4]:
+        raise ValueError("sd_kv4_verify_attention: queries and cache differ in dtype, head_dim, "
+                         "batch or device")
+    if kv.room is not None and q.desc.max_kv_len > kv.room:
         raise ValueError("sd_kv4_verify_attention: max_kv_len exceeds the cache's room")
-    out = _rows_out(out, q.q, "sd_kv4_verify_attention")
-    ws = _workspace(lambda: sd_kv4_attention_workspace_size(q, kv), q.q.device, workspace)
-    with _on(q.q):
-        _check(lib().sd_kv4_verify_attention(ctypes.byref(q.desc), _ptr(q.q),
-                                             ctypes.byref(kv.desc), kv.batch, _ptr(out), _ptr(ws),
-                                             ws.numel(), _ptr(dev_err), _stream(stream)),
+    out = _rows_out(out, t, "sd_kv4_verify_attention")
+    ws = _workspace(lambda: sd_kv4_attention_workspace_size(q, kv), t.device, workspace)
+    with _on(t):
+        _check(lib().sd_kv4_verify_attention(q.ref, _ptr(t), kv.ref, kv.row_shape[3], _ptr(out),
+                                             _ptr(ws), ws.numel(), _ptr(dev_err), _stream(stream)),
                "sd_kv4_verify_attention")
     return out

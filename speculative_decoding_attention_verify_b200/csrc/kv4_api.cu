@@ -132,7 +132,8 @@ sd_status status_of(cudaError_t e) { return e == cudaSuccess ? SD_OK : SD_ERR_CU
 
 struct Kv4Plan {
     int n_splits, simt_slots;  // CUDA-core engine
-    int ctas;                  // tensor-core engines (0: neither serves this call)
+    int ctas, tile;            // tensor-core engines (0 CTAs: neither serves this call)
+    bool whole;                // their CTAs share whole units
     bool tcgen05;              // which of the two
     size_t ws_bytes;
 };
@@ -153,11 +154,24 @@ sd_status plan_kv4(const sd_q_desc *q, const sd_kv4_desc *kv, int batch, Kv4Plan
     plan->n_splits = kv4_simt_splits(batch, kv->h_kv, (int)rows, q->max_kv_len);
     plan->simt_slots = plan->n_splits > 1 ? batch * kv->h_kv * plan->n_splits : 0;
     plan->tcgen05 = rows > kv4_mma_max_rows();
-    if (kv->dtype == SD_BF16 && rows <= kv4_tc_max_rows())
-        plan->ctas = plan->tcgen05 ? kv4_tc_ctas(batch, kv->h_kv, q->max_kv_len)
-                                   : kv4_mma_ctas(batch, kv->h_kv, q->max_kv_len);
+    if (kv->dtype == SD_BF16 && rows <= kv4_tc_max_rows()) {
+        int per_sm = 1;
+        if (plan->tcgen05)
+            kv4_tc_plan(&plan->tile, &per_sm);
+        else
+            kv4_mma_plan(kv->head_dim, (int)rows, &plan->tile, &per_sm);
+        const long long per_unit = ((long long)q->max_kv_len + plan->tile - 1) / plan->tile;
+        const long long units = (long long)batch * kv->h_kv;
+        const long long slots = (long long)device_sm_count() * per_sm;
+        // Up to four tiles per unit: whole units per CTA.  (A unit's further tiles cost about
+        // 1 us each; the merge is a launch of its own, 3 us, after partial results.)
+        plan->whole = per_unit <= 4;
+        const long long n = plan->whole ? units : units * per_unit;
+        plan->ctas = (int)(n < slots ? n : slots);
+    }
     // (whichever engine the pointers' alignment leaves)
-    const int slots = plan->simt_slots > 2 * plan->ctas ? plan->simt_slots : 2 * plan->ctas;
+    const int tc_slots = plan->whole ? 0 : 2 * plan->ctas;
+    const int slots = plan->simt_slots > tc_slots ? plan->simt_slots : tc_slots;
     plan->ws_bytes = (size_t)slots * rows * (kv->head_dim + 2) * sizeof(float);
     return SD_OK;
 }
@@ -285,6 +299,8 @@ sd_status sd_kv4_verify_attention(const sd_q_desc *q, const void *q_data, const 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (plan.ctas && aligned(q_data, 16) && aligned(out, 16)) {
         p.ctas = plan.ctas;
+        p.tile = plan.tile;
+        p.whole = plan.whole;
         p.n_slots = 2 * plan.ctas;
         p.wait_ns = wait_limit_ns();
         return status_of(plan.tcgen05 ? launch_kv4_tc(p, s) : launch_kv4_mma(p, s));

@@ -1,20 +1,19 @@
 // Shared by the kernels that read a 4-bit cache: sequences, row numbers, and the division of a
 // call's tiles over its CTAs.
 //
-// Tensor-core engines.  A unit is a (sequence, KV head); its positions are tiles of kKv4Tile.
+// Tensor-core engines.  A unit is a (sequence, KV head); its positions are tiles of p.tile.
 // All units' tiles, in (sequence, KV head) order, form one list of T tiles, counted on the device
 // from the actual lengths, and CTA c of G takes tiles [c T / G, (c+1) T / G) of it, so a ragged
 // batch is spread as evenly as an equal one whatever the hints say.  A unit inside one CTA's
 // range gets its output directly.  Otherwise the CTA that starts it writes partial slot 2c + 1
 // and each CTA that continues it slot 2c (of one CTA's units only the first can be continued and
-// only the last left open), and kv4_merge_kernel joins them in CTA order.
+// only the last left open), and kv4_merge_kernel joins them in CTA order.  With p.whole the CTAs
+// share the units instead, each a range of whole ones: nothing is left to join.
 #pragma once
 
 #include "sd_internal.h"
 
 namespace sd {
-
-constexpr int kKv4Tile = 128;
 
 // Sequence b of a 4-bit attention call: its rows and length; false (and *bad for a violated
 // hint) when it has no work.
@@ -33,7 +32,7 @@ __device__ __forceinline__ bool kv4_sequence(const Kv4Params &p, int b, int &q0,
 __device__ __forceinline__ int kv4_tiles(const Kv4Params &p, int b) {
     int q0, n_q, kv_len;
     bool bad;
-    return kv4_sequence(p, b, q0, n_q, kv_len, bad) ? (kv_len + kKv4Tile - 1) / kKv4Tile : 0;
+    return kv4_sequence(p, b, q0, n_q, kv_len, bad) ? (kv_len + p.tile - 1) / p.tile : 0;
 }
 
 // Row number of position j of (b, h), or -1 when its page is outside the pool.
@@ -117,16 +116,18 @@ static __device__ __noinline__ int kv4_next_sequence(const Kv4Params &p, int b) 
 struct Kv4Cursor {
     int b, g, t, tiles;
     int q0, n_q, kv_len;
-    // Sequence b or the next one with work (b = batch at the end).
+    // Sequence b at head g, or the next one with work (b = batch at the end).
     __device__ __forceinline__ void load(const Kv4Params &p) {
+        const int from = b;
         b = kv4_next_sequence(p, b);
+        if (b != from) g = 0;
         tiles = 1;
         kv_len = 0;
         if (b >= p.batch) return;
         q0 = __ldg(p.q_start + b);
         n_q = __ldg(p.q_start + b + 1) - q0;
         kv_len = __ldg(p.kv_len + b);
-        tiles = (kv_len + kKv4Tile - 1) / kKv4Tile;
+        tiles = (kv_len + p.tile - 1) / p.tile;
     }
     // n tiles on, within the unit or to the start of the next one.
     __device__ __forceinline__ void skip(const Kv4Params &p, int n) {
@@ -154,7 +155,7 @@ __device__ __forceinline__ Kv4Cursor kv4_first(const Kv4Params &p, long long *s_
     constexpr int W = NT / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long total = 0, unused;
-    kv4_count<NT>(p, 0, s_red, total, unused);
+    if (!p.whole) kv4_count<NT>(p, 0, s_red, total, unused);
     if (blockIdx.x == 0)
         for (int i = tid; i < p.batch; i += NT) {
             int q0, n_q, kv_len;
@@ -162,9 +163,26 @@ __device__ __forceinline__ Kv4Cursor kv4_first(const Kv4Params &p, long long *s_
             if (!kv4_sequence(p, i, q0, n_q, kv_len, bad) && bad)
                 set_dev_err(p.dev_err, SD_DEVERR_SHAPE);
         }
+    Kv4Cursor c{};
+    if (p.whole) {
+        const long long units = (long long)p.batch * p.h_kv;
+        const long long u0 = units * blockIdx.x / p.ctas, u1 = units * (blockIdx.x + 1) / p.ctas;
+        long long n = 0;
+        for (long long u = u0 + tid; u < u1; u += NT) n += kv4_tiles(p, (int)(u / p.h_kv));
+        n = warp_sum_ll(n);
+        __syncthreads();  // (the last use of s_red)
+        if (lane == 0) s_red[warp] = n;
+        __syncthreads();
+        lo = hi = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) hi += s_red[w];
+        c.b = (int)(u0 / p.h_kv);
+        c.g = (int)(u0 % p.h_kv);
+        if (hi > 0) c.load(p);
+        return c;
+    }
     const long long all = total * p.h_kv;
     const int ctas = kv4_ctas(p, all);
-    Kv4Cursor c{};
     lo = hi = 0;
     if ((int)blockIdx.x >= ctas) return c;
     lo = all * blockIdx.x / ctas;

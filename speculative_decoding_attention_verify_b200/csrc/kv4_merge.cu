@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const Kv4Params p) 
         long long total, before;
         kv4_count<kThreads>(p, b, s_red, total, before);
         total *= p.h_kv;
-        const int tiles = (kv_len + kKv4Tile - 1) / kKv4Tile;
+        const int tiles = (kv_len + p.tile - 1) / p.tile;
         const long long base = before * p.h_kv + (long long)g * tiles;
         const int ctas = kv4_ctas(p, total), c0 = kv4_cta_of(base, total, ctas);
         n = kv4_cta_of(base + tiles - 1, total, ctas) - c0 + 1;

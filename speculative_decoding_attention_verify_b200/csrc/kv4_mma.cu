@@ -22,12 +22,19 @@
 // one 8x8 transpose per 8 positions.  (mma.sync runs at 1,024 products per cycle per SM here, a
 // quarter of tcgen05's rate; at 8 rows that is a third of the time that a tile takes from HBM.)
 //
-// Work.  Two CTAs of 8 warps per SM; the CTAs share all units' tiles evenly (kv4_common.cuh) and
-// of a tile every warp takes 16 positions, one page.  Each warp streams its own positions through
-// its own ring of cp.async stages, with its page numbers looked up one stage further ahead, and
-// keeps its own running maximum, sums and O^T; there is no block-wide step until a unit ends,
-// where the warps are merged pairwise through shared memory.  The maximum moves only when a score
-// exceeds it by more than 2^8 (one vote per 16 positions; the weights stay below 256).
+// Work.  The CTAs share all units' tiles evenly (kv4_common.cuh).  A CTA's 8 warps are row blocks
+// (up to 8 NT rows each, NT = 1, 2 or 4) x slots of positions: of every tile a warp takes the 32
+// positions (two pages) of its slot for the rows of its block.  Warps of one slot expand the same
+// codes each for itself: with 32 rows to use them the expansion is a third of the work, and no
+// warp ever waits for another.  Each warp streams its positions through its own two cp.async
+// stages, with its page numbers looked up a stage further ahead, and keeps its own running maxima,
+// sums and O^T; there is no block-wide step until a unit ends, where the slots are merged pairwise
+// through shared memory.  The maximum moves only when a score exceeds it by more than 2^16 (one
+// vote per 32 positions; a weight stays finite in bf16 far beyond that).
+// Query fragments are registers for NT = 1; for more they are read from shared memory, once for
+// both pages.
+#include <type_traits>
+
 #include "kv4_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -40,22 +47,29 @@ using tc::saddr;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtasPerSm = 2;
-constexpr float kGrow = 8.0f;
-static_assert(kWarps * kPageSize == kKv4Tile, "a tile is one page per warp");
+constexpr int kPos = 32;       // positions of a warp per tile
+constexpr int kStages = 2;
+constexpr float kGrow = 16.0f;
+
+// CTAs per SM: registers of O^T decide.
+constexpr int ctas_per_sm(int nt) { return nt < 4 ? 2 : 1; }
 
 template <int D, int NT>
 struct MmaCfg {
-    static constexpr int kRow = D / 2;                    // bytes of a row's codes
-    static constexpr int kBlock = kPageSize * kRow;       // codes of one warp's positions
-    static constexpr int kStageBytes = 2 * kBlock + 128;  // K, V, parameters
-    static constexpr int kStages = 4;
+    static constexpr int kRow = D / 2;                     // bytes of a row's codes
+    static constexpr int kPage = kPageSize * kRow;         // codes of a page
+    static constexpr int kPageBytes = 2 * kPage + 128;     // K, V, parameters
+    static constexpr int kStageBytes = 2 * kPageBytes;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
-    static constexpr int kMt = D / 16;                    // channel tiles of O^T
-    static constexpr int kOFloats = kMt * NT * 4;         // O^T values of a lane
+    static constexpr int kMt = D / 16;                     // channel tiles of O^T, k steps of S^T
+    static constexpr int kOFloats = kMt * NT * 4;          // O^T values of a lane
     static constexpr int kPart = (kOFloats + 6 * NT) * 32;  // floats of one warp's partial
-    static constexpr int kSmem = kRing + kWarps / 2 * kPart * 4;
+    // query fragments: registers for NT = 1, of one row block for 2, of up to four for 4
+    static constexpr int kQ = kRing + kWarps / 2 * kPart * 4;
+    static constexpr int kSmem = kQ + (NT == 1 ? 0 : NT == 2 ? 1 : 4) * NT * kMt * 256;
 };
+static_assert(2 * (MmaCfg<128, 2>::kSmem + 1024) <= 227 * 1024, "two CTAs per SM");
+static_assert(MmaCfg<128, 4>::kSmem <= 226 * 1024, "shared memory");
 
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, int n) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
@@ -104,19 +118,22 @@ __device__ __forceinline__ int m_of(int r) { return (r & 8) | ((r & 3) << 1) | (
 __device__ __forceinline__ int pos_of(int m) { return (m & 8) | ((m & 1) << 2) | ((m >> 1) & 3); }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
+kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
     pdl_trigger();  // (see launch_pdl)
     pdl_wait();
     using C = MmaCfg<D, NT>;
     constexpr unsigned FULL = 0xffffffffu;
-    constexpr int kS = C::kStages;
-    constexpr int kKs = D / 16;  // k steps of S^T, and channel tiles of O^T
-    constexpr int kW = D / 32;   // 8-code words of a lane's share of a key
+    constexpr int kKs = C::kMt;
+    constexpr int kW = D / 32;  // 8-code words of a lane's share of a key
+    constexpr bool kQRegs = NT == 1;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_red[2 * kThreads / 32];
     __shared__ Kv4Start s_start;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gq = lane >> 2, t4 = lane & 3;
+    const int slots = p.tile / kPos, blocks = kWarps / slots;  // position slots, row blocks
+    const int rb = warp % blocks, slot = warp / blocks;
 
     long long lo, hi;
     Kv4Cursor cc = kv4_first<kThreads>(p, s_red, &s_start, lo, hi);  // next tile to compute
@@ -124,238 +141,316 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_mma_kernel(const __g
     Kv4Cursor pc = cc;  // next tile to copy
     const int n_my = (int)(hi - lo);
 
-    const uint32_t ring = saddr(smem) + warp * kS * C::kStageBytes;
-    // Page of the warp's positions of cursor c (contiguous caches: 0); -1: nothing to read.
-    auto page_of = [&](const Kv4Cursor &c) {
-        const int j0 = c.t * kKv4Tile + warp * kPageSize;
-        if (j0 >= c.kv_len) return -1;
-        return p.page_size ? __ldg(p.block_table + (int64_t)c.b * p.max_pages + (j0 >> 4)) : 0;
+    // ---- copies ----
+    const uint8_t *ring_p = smem + warp * kStages * C::kStageBytes;
+    const uint32_t ring = saddr(ring_p);
+    constexpr int Q = C::kRow / 16;  // 16-byte chunks of a row
+    // Where 16-byte chunk x of a page's codes goes: K rows in fragment order; V rows in place, the
+    // chunks of every second pair of rows swapped pairwise (a fragment's four rows then differ in
+    // banks).
+    auto k_at = [](int x) { return m_of(x / Q) * C::kRow + (x % Q) * 16; };
+    auto v_at = [](int x) {
+        const int r = x / Q;
+        return C::kPage + r * C::kRow + (D == 128 ? (x % Q) ^ (r & 2) : x % Q) * 16;
     };
-    int page = page_of(pc);
+    const uint32_t par_at = 2 * C::kPage + (lane & 16) * 4 + m_of(lane & 15) * 4;
+    const uint32_t *par_src = (lane < 16 ? p.kp : p.vp) + (lane & 15);
+    int pages[2];
+    auto look_up = [&]() {  // pages of the next tile to copy
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = pc.t * p.tile + slot * kPos + i * kPageSize;
+            pages[i] = p.page_size && j < pc.kv_len
+                           ? __ldg(p.block_table + (int64_t)pc.b * p.max_pages + (j >> 4))
+                           : 0;
+        }
+    };
+    look_up();
     int copied = 0;
     auto copy_next = [&]() {
         if (copied < n_my) {
-            const int j0 = pc.t * kKv4Tile + warp * kPageSize;
-            int n = pc.kv_len - j0;  // positions of this block
-            if (n > 0) {
-                int64_t row0 = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h + j0;
-                if (p.page_size) {
-                    row0 = ((int64_t)page * p.h_kv + pc.g) * kPageSize;
-                    if (page < 0 || page >= p.num_pages) {
-                        if (lane == 0) set_dev_err(p.dev_err, SD_DEVERR_PAGE);
-                        n = 0;  // (zeros, as the bf16 kernels' out-of-range boxes)
-                        row0 = 0;
+            const int j0 = pc.t * p.tile + slot * kPos;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = j0 + i * kPageSize;
+                int n = pc.kv_len - j;  // positions of this page
+                if (n > 0) {
+                    int64_t row0 = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h + j;
+                    if (p.page_size) {
+                        row0 = ((int64_t)pages[i] * p.h_kv + pc.g) * kPageSize;
+                        if (pages[i] < 0 || pages[i] >= p.num_pages) {
+                            if (lane == 0) set_dev_err(p.dev_err, SD_DEVERR_PAGE);
+                            n = 0;  // (zeros, as the bf16 kernels' out-of-range boxes)
+                            row0 = 0;
+                        }
+                    }
+                    const uint32_t dst =
+                        ring + (copied % kStages) * C::kStageBytes + i * C::kPageBytes;
+                    if (n >= kPageSize) {
+                        const int64_t off = row0 * C::kRow + lane * 16;
+#pragma unroll
+                        for (int k = 0; k < C::kPage / 512; ++k) {
+                            cp_async16(dst + k_at(lane + 32 * k), p.k + off + 512 * k);
+                            cp_async16(dst + v_at(lane + 32 * k), p.v + off + 512 * k);
+                        }
+                        cp_async4z(dst + par_at, par_src + row0, 4);
+                    } else {  // the end of the sequence: zeros past it
+#pragma unroll
+                        for (int k = 0; k < C::kPage / 512; ++k) {
+                            const int x = lane + 32 * k;
+                            const bool in = x / Q < n;
+                            const int64_t off = row0 * C::kRow + (in ? x : 0) * 16;
+                            cp_async16z(dst + k_at(x), p.k + off, in ? 16 : 0);
+                            cp_async16z(dst + v_at(x), p.v + off, in ? 16 : 0);
+                        }
+                        const bool in = (lane & 15) < n;
+                        cp_async4z(dst + par_at, in ? par_src + row0 : par_src - (lane & 15),
+                                   in ? 4 : 0);
                     }
                 }
-                const uint32_t dst = ring + (copied % kS) * C::kStageBytes;
-#pragma unroll
-                for (int i = 0; i < C::kBlock / 512; ++i) {
-                    const int x = lane + 32 * i;
-                    const int r = x / (C::kRow / 16), q = x % (C::kRow / 16);
-                    const bool in = r < n;
-                    const int64_t off = (row0 + (in ? r : 0)) * C::kRow + q * 16;
-                    cp_async16z(dst + m_of(r) * C::kRow + q * 16, p.k + off, in ? 16 : 0);
-                    const int qv = D == 128 ? q ^ (r & 2) : q;
-                    cp_async16z(dst + C::kBlock + r * C::kRow + qv * 16, p.v + off, in ? 16 : 0);
-                }
-                const int r = lane & 15;
-                const bool in = r < n;
-                cp_async4z(dst + 2 * C::kBlock + (lane & 16) * 4 + m_of(r) * 4,
-                           (lane < 16 ? p.kp : p.vp) + row0 + (in ? r : 0), in ? 4 : 0);
             }
             ++copied;
             pc.next(p);
-            if (copied < n_my) page = page_of(pc);
+            if (copied < n_my) look_up();
         }
         cp_async_commit();
     };
-#pragma unroll
-    for (int i = 0; i < kS - 1; ++i) copy_next();
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) copy_next();
 
+    uint2 *s_q = reinterpret_cast<uint2 *>(smem + C::kQ) + rb * NT * kKs * 32;
     int done = 0;
+#pragma unroll 1
     while (done < n_my) {
         // ---- a unit's share: tiles [cc.t, cc.t + n_seg) of unit (cc.b, cc.g) ----
         const int n_seg = min(cc.tiles - cc.t, n_my - done);
         const bool starts = cc.t == 0, ends = cc.t + n_seg == cc.tiles;
         const int G = p.group, R = cc.n_q * G, kv_len = cc.kv_len;
-        // the last position that query row 0 sees: blocks up to it need no mask
+        const int r_base = rb * 8 * NT;  // first row of the block
+        // the last position that query row 0 sees: positions up to it need no mask
         const int first_limit = kv_len - cc.n_q;
-        uint32_t qb[NT][kKs][2];
-        float qs[NT][2];   // sum of a column's query channels
-        int limit[NT][2];  // last visible position of columns 2t, 2t + 1
+        uint32_t qb[kQRegs ? kKs : 1][2];
+        float2 qs[NT];  // sums of the query channels of columns 2t, 2t + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = nt * 8 + gq;
+            const int r = r_base + nt * 8 + gq;
+            const bool has = r < R;
             const uint4 *src = reinterpret_cast<const uint4 *>(
                 static_cast<const unsigned short *>(p.q) +
-                ((int64_t)(cc.q0 + (r < R ? r / G : 0)) * p.h_q + cc.g * G + (r < R ? r % G : 0)) * D +
+                ((int64_t)(cc.q0 + (has ? r / G : 0)) * p.h_q + cc.g * G + (has ? r % G : 0)) * D +
                 t4 * (D / 4));
             float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kW; ++w) {
-                const uint4 x = r < R ? __ldg(src + w) : make_uint4(0u, 0u, 0u, 0u);
-                qb[nt][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);
-                qb[nt][2 * w][1] = __byte_perm(x.x, x.z, 0x7632);
-                qb[nt][2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);
-                qb[nt][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);
+                const uint4 x = has ? __ldg(src + w) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t f0 = __byte_perm(x.x, x.z, 0x5410), f1 = __byte_perm(x.x, x.z, 0x7632);
+                const uint32_t f2 = __byte_perm(x.y, x.w, 0x5410), f3 = __byte_perm(x.y, x.w, 0x7632);
+                if constexpr (kQRegs) {
+                    qb[2 * w][0] = f0;
+                    qb[2 * w][1] = f1;
+                    qb[2 * w + 1][0] = f2;
+                    qb[2 * w + 1][1] = f3;
+                } else if (slot == 0) {
+                    s_q[((2 * w) * NT + nt) * 32 + lane] = make_uint2(f0, f1);
+                    s_q[((2 * w + 1) * NT + nt) * 32 + lane] = make_uint2(f2, f3);
+                }
                 sum += bf16_lo(x.x) + bf16_hi(x.x) + bf16_lo(x.y) + bf16_hi(x.y) + bf16_lo(x.z) +
                        bf16_hi(x.z) + bf16_lo(x.w) + bf16_hi(x.w);
             }
             sum += __shfl_xor_sync(FULL, sum, 1);
             sum += __shfl_xor_sync(FULL, sum, 2);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                qs[nt][c] = __shfl_sync(FULL, sum, (2 * t4 + c) * 4);
-                const int n = nt * 8 + 2 * t4 + c;
-                limit[nt][c] = n < R ? first_limit + n / G : -1;
-            }
+            qs[nt].x = __shfl_sync(FULL, sum, (2 * t4) * 4);
+            qs[nt].y = __shfl_sync(FULL, sum, (2 * t4 + 1) * 4);
         }
-        float o[kKs][NT][4], m[NT][2], l[NT][2], cr[NT][2];
+        // (the merge's barriers at the end of a share keep the fragments until all have read them)
+        if (!kQRegs) __syncthreads();
+        float o[kKs][NT][4], m[NT][2];
+        float2 l2[NT], cr2[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int mt = 0; mt < kKs; ++mt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                m[nt][c] = -INFINITY;
-                l[nt][c] = cr[nt][c] = 0.f;
-            }
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l2[nt] = cr2[nt] = make_float2(0.f, 0.f);
         }
-        for (int it = 0; it < n_seg; ++it, ++done) {
-            copy_next();
-            cp_async_wait<kS - 1>();
-            __syncwarp();
-            const int j0 = (cc.t + it) * kKv4Tile + warp * kPageSize;
-            if (j0 < kv_len) {
-                const uint8_t *st = smem + (warp * kS + done % kS) * C::kStageBytes;
-                // ---- S^T = K Q^T ----
-                uint32_t kw[2][kW];
+        // One page pair at j0 (instantiated apart for positions that need no mask).
+        auto step = [&](const uint8_t *st, int j0, auto masked) {
+            constexpr bool kMasked = decltype(masked)::value;
+            // ---- S^T = K Q^T: s[page][nt] holds positions pos_of(g), pos_of(g) + 8 ----
+            float s[2][NT][4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint8_t *src = st + (gq + 8 * i) * C::kRow + t4 * (C::kRow / 4);
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i][nt][e] = 0.f;
+            uint32_t kw[2][2][kW];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint8_t *src =
+                        st + i * C::kPageBytes + (gq + 8 * h) * C::kRow + t4 * (C::kRow / 4);
                     if constexpr (D == 128) {
                         const uint4 x = *reinterpret_cast<const uint4 *>(src);
-                        kw[i][0] = x.x;
-                        kw[i][1] = x.y;
-                        kw[i][kW - 2] = x.z;
-                        kw[i][kW - 1] = x.w;
+                        kw[i][h][0] = x.x;
+                        kw[i][h][1] = x.y;
+                        kw[i][h][kW - 2] = x.z;
+                        kw[i][h][kW - 1] = x.w;
                     } else {
                         const uint2 x = *reinterpret_cast<const uint2 *>(src);
-                        kw[i][0] = x.x;
-                        kw[i][1] = x.y;
+                        kw[i][h][0] = x.x;
+                        kw[i][h][1] = x.y;
                     }
                 }
-                float s[NT][4], s2[NT][4];  // two chains of products
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int w = 0; w < kW; ++w) {
+                uint2 f[2][NT];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
-#pragma unroll
-                for (int w = 0; w < kW; ++w) {
-                    const uint32_t a0 = codes_at<0>(kw[0][w]), a1 = codes_at<0>(kw[1][w]);
-                    const uint32_t a2 = codes_at<1>(kw[0][w]), a3 = codes_at<1>(kw[1][w]);
-                    const uint32_t b0 = codes_at<2>(kw[0][w]), b1 = codes_at<2>(kw[1][w]);
-                    const uint32_t b2 = codes_at<3>(kw[0][w]), b3 = codes_at<3>(kw[1][w]);
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma16816(s[nt], a0, a1, a2, a3, qb[nt][2 * w][0], qb[nt][2 * w][1]);
-                        mma16816(s2[nt], b0, b1, b2, b3, qb[nt][2 * w + 1][0], qb[nt][2 * w + 1][1]);
+                        if constexpr (kQRegs)
+                            f[h][nt] = make_uint2(qb[2 * w + h][0], qb[2 * w + h][1]);
+                        else
+                            f[h][nt] = s_q[((2 * w + h) * NT + nt) * 32 + lane];
                     }
-                }
-                const uint32_t *par = reinterpret_cast<const uint32_t *>(st + 2 * C::kBlock);
-                const uint32_t kp0 = par[gq], kp1 = par[gq + 8];
-                const uint32_t vp0 = par[16 + gq], vp1 = par[24 + gq];
-                // scores in log2 units: s[0], s[1] at position pos_of(g), s[2], s[3] at g + 8
-                const float ks0 = param_scale(kp0) * p.scale_log2, ks1 = param_scale(kp1) * p.scale_log2;
-                const float kl0 = fmaf(param_low(kp0), p.scale_log2, -16.f * ks0);
-                const float kl1 = fmaf(param_low(kp1), p.scale_log2, -16.f * ks1);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        s[nt][c] = fmaf(ks0, s[nt][c] + s2[nt][c], kl0 * qs[nt][c]);
-                        s[nt][2 + c] = fmaf(ks1, s[nt][2 + c] + s2[nt][2 + c], kl1 * qs[nt][c]);
-                    }
-                const bool whole = j0 + kPageSize - 1 <= first_limit;
-                const int pa = j0 + pos_of(gq), pb = pa + 8;
-                if (!whole) {
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t x = kw[i][0][w], y = kw[i][1][w];
+                    const uint32_t a0 = codes_at<0>(x), a1 = codes_at<0>(y);
+                    const uint32_t a2 = codes_at<1>(x), a3 = codes_at<1>(y);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
+                        mma16816(s[i][nt], a0, a1, a2, a3, f[0][nt].x, f[0][nt].y);
+                    const uint32_t b0 = codes_at<2>(x), b1 = codes_at<2>(y);
+                    const uint32_t b2 = codes_at<3>(x), b3 = codes_at<3>(y);
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            if (pa > limit[nt][c]) s[nt][c] = -INFINITY;
-                            if (pb > limit[nt][c]) s[nt][2 + c] = -INFINITY;
-                        }
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16816(s[i][nt], b0, b1, b2, b3, f[1][nt].x, f[1][nt].y);
                 }
-                bool grow = false;
+            }
+            // ---- exponents: scores in log2 units less the maximum ----
+            float2 nm[NT];  // (before a column's first visible position its maximum counts as 0)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                nm[nt] = make_float2(m[nt][0] == -INFINITY ? 0.f : -m[nt][0],
+                                     m[nt][1] == -INFINITY ? 0.f : -m[nt][1]);
+            bool grow = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t *par =
+                    reinterpret_cast<const uint32_t *>(st + i * C::kPageBytes + 2 * C::kPage);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t kp = par[gq + 8 * h];
+                    const float ks = param_scale(kp) * p.scale_log2;
+                    const float kl = fmaf(param_low(kp), p.scale_log2, -16.f * ks);
+                    const float2 ks2 = make_float2(ks, ks), kl2 = make_float2(kl, kl);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float2 x =
+                            __ffma2_rn(make_float2(s[i][nt][2 * h], s[i][nt][2 * h + 1]), ks2,
+                                       __ffma2_rn(kl2, qs[nt], nm[nt]));
+                        s[i][nt][2 * h] = x.x;
+                        s[i][nt][2 * h + 1] = x.y;
+                    }
+                }
+            }
+            if constexpr (kMasked) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        grow |= fmaxf(s[nt][c], s[nt][2 + c]) > m[nt][c] + kGrow;
-                if (__any_sync(FULL, grow)) {
+                    for (int c = 0; c < 2; ++c) {
+                        // last visible position of the column (those past R see nothing)
+                        const int n = r_base + nt * 8 + 2 * t4 + c;
+                        const int limit = n < R ? first_limit + n / G : -1;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float f[2];
+                        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float x = fmaxf(s[nt][c], s[nt][2 + c]);
-                            x = fmaxf(x, __shfl_xor_sync(FULL, x, 4));
-                            x = fmaxf(x, __shfl_xor_sync(FULL, x, 8));
-                            x = fmaxf(x, __shfl_xor_sync(FULL, x, 16));
-                            x = fmaxf(x, m[nt][c]);
-                            f[c] = x == -INFINITY ? 1.f : ex2(m[nt][c] - x);
-                            m[nt][c] = x;
-                            l[nt][c] *= f[c];
-                            cr[nt][c] *= f[c];
-                        }
-#pragma unroll
-                        for (int mt = 0; mt < kKs; ++mt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[mt][nt][e] *= f[e & 1];
+                            for (int h = 0; h < 2; ++h)
+                                if (j0 + i * kPageSize + pos_of(gq) + 8 * h > limit)
+                                    s[i][nt][2 * h + c] = -INFINITY;
                     }
-                }
-                // ---- weights, and P^T in operand layout ----
-                const float vs0 = param_scale(vp0), vs1 = param_scale(vp1);
-                const float vl0 = fmaf(8.f, vs0, param_low(vp0)), vl1 = fmaf(8.f, vs1, param_low(vp1));
-                uint32_t pt[NT][2];
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    grow |= fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]),
+                                  fmaxf(s[1][nt][c], s[1][nt][2 + c])) >
+                            (m[nt][c] == -INFINITY ? -INFINITY : kGrow);
+            if (__any_sync(FULL, grow)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float w0[2], w1[2];
+                    float f[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float base = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
-                        const float e0 = ex2(s[nt][c] - base), e1 = ex2(s[nt][2 + c] - base);
-                        l[nt][c] += e0 + e1;
-                        w0[c] = e0 * vs0;
-                        w1[c] = e1 * vs1;
-                        float k0 = e0 * vl0, k1 = e1 * vl1;
-                        if (!whole) {  // a hidden position's NaN must not get through
-                            if (pa > limit[nt][c]) w0[c] = k0 = 0.f;
-                            if (pb > limit[nt][c]) w1[c] = k1 = 0.f;
+                        float x = fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]),
+                                        fmaxf(s[1][nt][c], s[1][nt][2 + c]));
+                        x = fmaxf(x, __shfl_xor_sync(FULL, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(FULL, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(FULL, x, 16));
+                        const bool up = x > (m[nt][c] == -INFINITY ? -INFINITY : kGrow);
+                        f[c] = up && m[nt][c] != -INFINITY ? ex2(-x) : 1.f;
+                        if (up) {
+                            m[nt][c] = (m[nt][c] == -INFINITY ? 0.f : m[nt][c]) + x;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                s[i][nt][c] -= x;
+                                s[i][nt][2 + c] -= x;
+                            }
                         }
-                        cr[nt][c] += k0 + k1;
                     }
-                    pt[nt][0] = transpose8(pack_bf16(w0[0], w0[1]));
-                    pt[nt][1] = transpose8(pack_bf16(w1[0], w1[1]));
+                    l2[nt] = __fmul2_rn(l2[nt], make_float2(f[0], f[1]));
+                    cr2[nt] = __fmul2_rn(cr2[nt], make_float2(f[0], f[1]));
+#pragma unroll
+                    for (int mt = 0; mt < kKs; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[mt][nt][e] *= f[e & 1];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint8_t *pg = st + i * C::kPageBytes;
+                const uint32_t *par = reinterpret_cast<const uint32_t *>(pg + 2 * C::kPage);
+                // ---- weights, and P^T in operand layout ----
+                uint32_t pt[NT][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t vp = par[16 + gq + 8 * h];
+                    const float vs = param_scale(vp), vl = fmaf(8.f, vs, param_low(vp));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float a = s[i][nt][2 * h], b = s[i][nt][2 * h + 1];
+                        float2 vs2 = make_float2(vs, vs), vl2 = make_float2(vl, vl);
+                        if constexpr (kMasked) {  // a hidden position's NaN must not get through
+                            if (a == -INFINITY) vs2.x = vl2.x = 0.f;
+                            if (b == -INFINITY) vs2.y = vl2.y = 0.f;
+                        }
+                        const float2 e = make_float2(ex2(a), ex2(b));
+                        l2[nt] = __fadd2_rn(l2[nt], e);
+                        cr2[nt] = __ffma2_rn(e, vl2, cr2[nt]);
+                        const float2 wv = __fmul2_rn(e, vs2);
+                        pt[nt][h] = transpose8(pack_bf16(wv.x, wv.y));
+                    }
                 }
                 // ---- O^T += V^T P^T ----
                 constexpr int kVw = D / 64;  // words of a lane's 8-channel groups per position
                 uint32_t vw[4][kVw];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = t4 + 4 * i;
+                for (int h = 0; h < 4; ++h) {
+                    const int r = t4 + 4 * h;
                     if constexpr (D == 128) {
-                        const int q = (gq >> 1) ^ (r & 2);
                         const uint2 x = *reinterpret_cast<const uint2 *>(
-                            st + C::kBlock + r * C::kRow + q * 16 + (gq & 1) * 8);
-                        vw[i][0] = x.x;
-                        vw[i][kVw - 1] = x.y;
+                            pg + C::kPage + r * C::kRow + ((gq >> 1) ^ (r & 2)) * 16 + (gq & 1) * 8);
+                        vw[h][0] = x.x;
+                        vw[h][kVw - 1] = x.y;
                     } else {
-                        vw[i][0] = *reinterpret_cast<const uint32_t *>(st + C::kBlock +
-                                                                       r * C::kRow + gq * 4);
+                        vw[h][0] = *reinterpret_cast<const uint32_t *>(pg + C::kPage + r * C::kRow +
+                                                                       gq * 4);
                     }
                 }
                 // channel D/8 g + 8 w + 4 h + c: tile 4 w + 2 h + c / 2, row g + 8 (c & 1)
@@ -367,20 +462,40 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_mma_kernel(const __g
                         const uint32_t y = __byte_perm(vw[2][w], vw[3][w], h ? 0x7632 : 0x5410);
                         const uint32_t a0 = sub24(codes_at<0>(x)), a1 = sub24(codes_at<1>(x));
                         const uint32_t a2 = sub24(codes_at<0>(y)), a3 = sub24(codes_at<1>(y));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816(o[4 * w + 2 * h][nt], a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
                         const uint32_t b0 = sub24(codes_at<2>(x)), b1 = sub24(codes_at<3>(x));
                         const uint32_t b2 = sub24(codes_at<2>(y)), b3 = sub24(codes_at<3>(y));
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma16816(o[4 * w + 2 * h][nt], a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
+                        for (int nt = 0; nt < NT; ++nt)
                             mma16816(o[4 * w + 2 * h + 1][nt], b0, b1, b2, b3, pt[nt][0], pt[nt][1]);
-                        }
                     }
+            }
+        };
+#pragma unroll 1
+        for (int it = 0; it < n_seg; ++it, ++done) {
+            copy_next();
+            cp_async_wait<kStages - 1>();
+            __syncwarp();
+            const int j0 = (cc.t + it) * p.tile + slot * kPos;
+            const uint8_t *st = ring_p + (done % kStages) * C::kStageBytes;
+            if (r_base < R) {
+                if (j0 + kPos - 1 <= first_limit)
+                    step(st, j0, std::false_type{});
+                else if (j0 < kv_len)  // (a second page past the end is masked as a whole)
+                    step(st, j0, std::true_type{});
             }
             __syncwarp();  // (the stage's next copies)
         }
-        // ---- end of the share: merge the warps ----
+        // ---- end of the share: merge the slots ----
+        float l[NT][2], cr[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+            l[nt][0] = l2[nt].x;
+            l[nt][1] = l2[nt].y;
+            cr[nt][0] = cr2[nt].x;
+            cr[nt][1] = cr2[nt].y;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -391,11 +506,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_mma_kernel(const __g
                 // (a sum that is NaN needs a finite maximum to survive a merge)
                 if (l[nt][c] != l[nt][c] && m[nt][c] == -INFINITY) m[nt][c] = 0.f;
             }
+        }
         float *part = reinterpret_cast<float *>(smem + C::kRing);
-#pragma unroll
-        for (int half = kWarps / 2; half > 0; half >>= 1) {
-            if (warp >= half && warp < 2 * half) {
-                float *d = part + (warp - half) * C::kPart + lane;
+#pragma unroll 1
+        for (int half = slots / 2; half > 0; half >>= 1) {
+            if (slot >= half && slot < 2 * half) {
+                float *d = part + (warp - half * blocks) * C::kPart + lane;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -411,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_mma_kernel(const __g
                 }
             }
             __syncthreads();
-            if (warp < half) {
+            if (slot < half) {
                 const float *d = part + warp * C::kPart + lane;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -436,12 +552,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_mma_kernel(const __g
             }
             __syncthreads();
         }
-        if (warp == 0) {
+        if (slot == 0) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int n = nt * 8 + 2 * t4 + c;
+                    const int n = r_base + nt * 8 + 2 * t4 + c;
                     if (n >= R) continue;
                     // this lane's channels [D/8 g, D/8 (g + 1)) of column n, in order
                     float x[D / 8];
@@ -462,19 +578,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_mma_kernel(const __g
                                                 pack_bf16(x[8 * i + 4] * inv, x[8 * i + 5] * inv),
                                                 pack_bf16(x[8 * i + 6] * inv, x[8 * i + 7] * inv));
                     } else {
-                        const int64_t slot = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
-                        float4 *dst = reinterpret_cast<float4 *>(kv4_slot_o(p, slot, n) + gq * (D / 8));
+                        const int64_t part_slot = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
+                        float4 *dst =
+                            reinterpret_cast<float4 *>(kv4_slot_o(p, part_slot, n) + gq * (D / 8));
 #pragma unroll
                         for (int i = 0; i < D / 32; ++i)
                             dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                         if (gq == 0) {
-                            float *ml = kv4_slot_ml(p, slot, n);
+                            float *ml = kv4_slot_ml(p, part_slot, n);
                             ml[0] = m[nt][c];
                             ml[1] = l[nt][c];
                         }
                     }
                 }
         }
+        // (one slot: nothing above keeps the next share's query fragments off this one's readers)
+        if (!kQRegs && slots == 1) __syncthreads();
         cc.skip(p, n_seg);
     }
     cp_async_wait<0>();
@@ -486,24 +605,30 @@ cudaError_t launch_t(const Kv4Params &p, cudaStream_t s) {
     cudaError_t e = set_max_dynamic_smem<kv4_mma_kernel<D, NT>>(bytes);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kv4_mma_kernel<D, NT>, dim3(p.ctas), dim3(kThreads), bytes, s, p);
-    return e != cudaSuccess ? e : launch_kv4_merge(p, s);
+    return e != cudaSuccess || p.whole ? e : launch_kv4_merge(p, s);
+}
+
+int row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+template <int D>
+cudaError_t launch_d(const Kv4Params &p, cudaStream_t s) {
+    const int nt = row_tiles(p.group * p.max_q_rows);
+    return nt == 1 ? launch_t<D, 1>(p, s) : nt == 2 ? launch_t<D, 2>(p, s) : launch_t<D, 4>(p, s);
 }
 
 }  // namespace
 
-int kv4_mma_max_rows() { return 16; }
+int kv4_mma_max_rows() { return 128; }
 
-// CTAs of a launch: no more than the tiles that the hints allow.
-int kv4_mma_ctas(int batch, int h_kv, int max_kv_len) {
-    const long long tiles = (long long)batch * h_kv * (((long long)max_kv_len + kKv4Tile - 1) / kKv4Tile);
-    const long long g = (long long)device_sm_count() * kCtasPerSm;
-    return (int)(tiles < g ? tiles : g);
+// Row blocks of 32 rows (1, 2 or 4 of them) leave 8, 4 or 2 slots of 32 positions to a tile.
+void kv4_mma_plan(int head_dim, int rows, int *tile, int *per_sm) {
+    (void)head_dim;
+    *tile = kPos * (rows <= 32 ? kWarps : rows <= 64 ? kWarps / 2 : kWarps / 4);
+    *per_sm = ctas_per_sm(row_tiles(rows));
 }
 
 cudaError_t launch_kv4_mma(const Kv4Params &p, cudaStream_t s) {
-    const bool one = p.group * p.max_q_rows <= 8;
-    if (p.head_dim == 128) return one ? launch_t<128, 1>(p, s) : launch_t<128, 2>(p, s);
-    return one ? launch_t<64, 1>(p, s) : launch_t<64, 2>(p, s);
+    return p.head_dim == 128 ? launch_d<128>(p, s) : launch_d<64>(p, s);
 }
 
 }  // namespace sd

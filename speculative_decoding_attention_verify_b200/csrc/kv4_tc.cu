@@ -42,7 +42,7 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;           // MMA M
-constexpr int kTile = kKv4Tile;      // positions per tile
+constexpr int kTile = 128;           // positions per tile (p.tile)
 constexpr int kExpandWarp = 4;       // first of eight
 constexpr int kExpandWarps = 8;
 constexpr int kSWarp = 12;
@@ -790,7 +790,7 @@ cudaError_t launch_t(const Kv4Params &p, cudaStream_t s) {
     cudaError_t e = set_max_dynamic_smem<kv4_tc_kernel<D, NCP>>(bytes);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kv4_tc_kernel<D, NCP>, dim3(p.ctas), dim3(kThreads), bytes, s, p);
-    return e != cudaSuccess ? e : launch_kv4_merge(p, s);
+    return e != cudaSuccess || p.whole ? e : launch_kv4_merge(p, s);
 }
 
 template <int D>
@@ -803,10 +803,9 @@ cudaError_t launch_d(const Kv4Params &p, cudaStream_t s) {
 
 int kv4_tc_max_rows() { return kRows; }
 
-int kv4_tc_ctas(int batch, int h_kv, int max_kv_len) {
-    const long long tiles = (long long)batch * h_kv * (((long long)max_kv_len + kTile - 1) / kTile);
-    const int sms = device_sm_count();
-    return (int)(tiles < sms ? tiles : sms);
+void kv4_tc_plan(int *tile, int *ctas_per_sm) {
+    *tile = kTile;
+    *ctas_per_sm = 1;
 }
 
 cudaError_t launch_kv4_tc(const Kv4Params &p, cudaStream_t s) {

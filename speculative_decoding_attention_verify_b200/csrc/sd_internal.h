@@ -241,6 +241,8 @@ struct Kv4Params {
     void *out;
     int n_splits;    // CUDA-core engine: splits of every sequence's positions
     int ctas;        // tensor-core engines: CTAs that share all units' tiles (0: CUDA cores)
+    int tile;        // positions of a tile
+    int whole;       // the CTAs share whole units, not tiles
     int n_slots;     // partial results that ws holds, [n_slots][group * max_q_rows] rows each
     float *ws;
     int32_t *dev_err;
@@ -249,10 +251,10 @@ struct Kv4Params {
 int kv4_simt_splits(int batch, int h_kv, int rows, int max_kv_len);
 cudaError_t launch_kv4_simt(const Kv4Params &p, cudaStream_t s);
 int kv4_mma_max_rows();  // rows per KV head of the register-expanding tensor-core engine
-int kv4_mma_ctas(int batch, int h_kv, int max_kv_len);
+void kv4_mma_plan(int head_dim, int rows, int *tile, int *ctas_per_sm);
 cudaError_t launch_kv4_mma(const Kv4Params &p, cudaStream_t s);
 int kv4_tc_max_rows();  // rows per KV head of the tcgen05 engine
-int kv4_tc_ctas(int batch, int h_kv, int max_kv_len);
+void kv4_tc_plan(int *tile, int *ctas_per_sm);
 cudaError_t launch_kv4_tc(const Kv4Params &p, cudaStream_t s);
 cudaError_t launch_kv4_merge(const Kv4Params &p, cudaStream_t s);
 

@@ -170,9 +170,13 @@ sd_status plan_kv4(const sd_q_desc *q, const sd_kv4_desc *kv, int batch, Kv4Plan
         plan->ctas = (int)(n < slots ? n : slots);
     }
     // (whichever engine the pointers' alignment leaves)
-    const int tc_slots = plan->whole ? 0 : 2 * plan->ctas;
-    const int slots = plan->simt_slots > tc_slots ? plan->simt_slots : tc_slots;
-    plan->ws_bytes = (size_t)slots * rows * (kv->head_dim + 2) * sizeof(float);
+    const size_t slot = (size_t)rows * (kv->head_dim + 2) * sizeof(float);
+    const size_t simt = plan->simt_slots * slot;
+    // (and the CTAs of every unit)
+    const size_t tc = !plan->ctas || plan->whole
+                          ? 0
+                          : 2 * plan->ctas * slot + (size_t)batch * kv->h_kv * 2 * sizeof(int32_t);
+    plan->ws_bytes = simt > tc ? simt : tc;
     return SD_OK;
 }
 

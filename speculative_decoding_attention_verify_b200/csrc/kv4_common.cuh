@@ -29,12 +29,6 @@ __device__ __forceinline__ bool kv4_sequence(const Kv4Params &p, int b, int &q0,
     return !bad;
 }
 
-__device__ __forceinline__ int kv4_tiles(const Kv4Params &p, int b) {
-    int q0, n_q, kv_len;
-    bool bad;
-    return kv4_sequence(p, b, q0, n_q, kv_len, bad) ? (kv_len + p.tile - 1) / p.tile : 0;
-}
-
 // Row number of position j of (b, h), or -1 when its page is outside the pool.
 __device__ __forceinline__ int64_t kv4_row(const Kv4Params &p, int b, int h, int j) {
     if (p.page_size == 0)
@@ -50,46 +44,15 @@ __device__ __forceinline__ int64_t kv4_row(const Kv4Params &p, int b, int h, int
 __device__ __forceinline__ float param_scale(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float param_low(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-__device__ __forceinline__ long long warp_sum_ll(long long x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-
-// Tiles (of one KV head) of all sequences and of those before sequence b.  Every thread of the
-// block calls it; s_red holds 2 * NT / 32 values.
-template <int NT>
-__device__ __forceinline__ void kv4_count(const Kv4Params &p, int b, long long *s_red,
-                                          long long &total, long long &before) {
-    long long t = 0, u = 0;
-    for (int i = threadIdx.x; i < p.batch; i += NT) {
-        const int n = kv4_tiles(p, i);
-        t += n;
-        if (i < b) u += n;
-    }
-    t = warp_sum_ll(t);
-    u = warp_sum_ll(u);
-    if ((threadIdx.x & 31) == 0) {
-        s_red[2 * (threadIdx.x >> 5)] = t;
-        s_red[2 * (threadIdx.x >> 5) + 1] = u;
-    }
-    __syncthreads();
-    total = before = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-        total += s_red[2 * w];
-        before += s_red[2 * w + 1];
-    }
-}
-
 // CTAs that take part: no more than there are tiles, so that each has one at least.
 __device__ __forceinline__ int kv4_ctas(const Kv4Params &p, long long total) {
     return (int)(total < p.ctas ? total : p.ctas);
 }
 
-// CTA of G that holds tile x of T.
-__device__ __forceinline__ int kv4_cta_of(long long x, long long total, int ctas) {
-    return (int)(((x + 1) * ctas - 1) / total);
+// The CTAs that hold a unit's first and last tile, written by those CTAs for the merge.
+__device__ __forceinline__ int2 *kv4_unit_ctas(const Kv4Params &p) {
+    return reinterpret_cast<int2 *>(p.ws + (int64_t)p.n_slots * p.group * p.max_q_rows *
+                                               (p.head_dim + 2));
 }
 
 // Where partial slot `slot` keeps local row lr: its outputs, and its (maximum in log2 units, sum).
@@ -143,57 +106,46 @@ struct Kv4Cursor {
 };
 
 struct Kv4Start {
-    int b;
-    long long before;  // tiles of one KV head before sequence b
+    Kv4Cursor c;       // at tile 0 of KV head 0 of its sequence
+    long long before;  // tiles of one KV head before that sequence
 };
 
-// The CTA's range [lo, hi) of the list of tiles, and the cursor at lo.  Every thread of the block
-// calls it; s_red holds 2 * NT / 32 values.  CTA 0 reports violated hints.
+// The CTA's tiles: [lo, hi) of the list (p.whole: hi - lo of its own units), and the cursor at the
+// first.  Every thread of the block calls it; s_red holds NT / 32 values.  The sequences are read
+// once, NT at a time (one round of loads for up to NT of them), and CTA 0 reports violated hints.
 template <int NT>
 __device__ __forceinline__ Kv4Cursor kv4_first(const Kv4Params &p, long long *s_red,
                                                Kv4Start *s_start, long long &lo, long long &hi) {
     constexpr int W = NT / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long total = 0, unused;
-    if (!p.whole) kv4_count<NT>(p, 0, s_red, total, unused);
-    if (blockIdx.x == 0)
-        for (int i = tid; i < p.batch; i += NT) {
-            int q0, n_q, kv_len;
-            bool bad;
-            if (!kv4_sequence(p, i, q0, n_q, kv_len, bad) && bad)
-                set_dev_err(p.dev_err, SD_DEVERR_SHAPE);
-        }
-    Kv4Cursor c{};
-    if (p.whole) {
-        const long long units = (long long)p.batch * p.h_kv;
-        const long long u0 = units * blockIdx.x / p.ctas, u1 = units * (blockIdx.x + 1) / p.ctas;
-        long long n = 0;
-        for (long long u = u0 + tid; u < u1; u += NT) n += kv4_tiles(p, (int)(u / p.h_kv));
-        n = warp_sum_ll(n);
-        __syncthreads();  // (the last use of s_red)
-        if (lane == 0) s_red[warp] = n;
-        __syncthreads();
-        lo = hi = 0;
-#pragma unroll
-        for (int w = 0; w < W; ++w) hi += s_red[w];
-        c.b = (int)(u0 / p.h_kv);
-        c.g = (int)(u0 % p.h_kv);
-        if (hi > 0) c.load(p);
-        return c;
-    }
-    const long long all = total * p.h_kv;
-    const int ctas = kv4_ctas(p, all);
-    lo = hi = 0;
-    if ((int)blockIdx.x >= ctas) return c;
-    lo = all * blockIdx.x / ctas;
-    hi = all * (blockIdx.x + 1) / ctas;
-    // the sequence that holds tile lo: prefix sums over NT sequences at a time
-    const long long want = lo / p.h_kv;  // (before b) <= want < (before b + 1)
-    long long base = 0;
-    for (int i0 = 0; i0 < p.batch && base <= want; i0 += NT) {
+    const long long units = (long long)p.batch * p.h_kv;
+    const long long u0 = units * blockIdx.x / p.ctas, u1 = units * (blockIdx.x + 1) / p.ctas;
+    // pass 0: the total (p.whole: the tiles of units [u0, u1)); pass 1: the sequence of tile lo.
+    // One chunk of sequences needs one pass: every thread keeps its own.
+    Kv4Cursor mine{};
+    long long total = 0;
+    int n = 0;
+    for (int i0 = 0; i0 < p.batch; i0 += NT) {
         const int i = i0 + tid;
-        const int n = i < p.batch ? kv4_tiles(p, i) : 0;
+        n = 0;
+        if (i < p.batch) {
+            bool bad;
+            if (kv4_sequence(p, i, mine.q0, mine.n_q, mine.kv_len, bad))
+                n = (mine.kv_len + p.tile - 1) / p.tile;
+            if (bad && blockIdx.x == 0) set_dev_err(p.dev_err, SD_DEVERR_SHAPE);
+        }
+        mine.b = i;
+        mine.tiles = n;
         long long x = n;
+        if (p.whole) {
+            const long long a = (long long)i * p.h_kv, b = a + p.h_kv;
+            const long long in = (u1 < b ? u1 : b) - (u0 > a ? u0 : a);
+            x = in > 0 ? x * in : 0;
+        }
+        total += x;
+    }
+    // sums before this thread's sequence within the last chunk, and the total
+    auto scan = [&](long long x, long long &sum) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -202,21 +154,68 @@ __device__ __forceinline__ Kv4Cursor kv4_first(const Kv4Params &p, long long *s_
         __syncthreads();  // (the last use of s_red)
         if (lane == 31) s_red[warp] = x;
         __syncthreads();
-        long long chunk = 0, mine = base + x - n;
+        sum = 0;
+        long long before = x;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            if (w < warp) mine += s_red[w];
-            chunk += s_red[w];
+            if (w < warp) before += s_red[w];
+            sum += s_red[w];
         }
-        if (n > 0 && mine <= want && want < mine + n) {
-            s_start->b = i;
-            s_start->before = mine;
+        return before;
+    };
+    long long sum;
+    long long upto = scan(total, sum);
+    Kv4Cursor c{};
+    lo = hi = 0;
+    if (p.whole) {
+        hi = sum;
+        if (hi == 0) return c;
+        c.b = (int)(u0 / p.h_kv);
+        c.g = (int)(u0 % p.h_kv);
+        if (p.batch <= NT) {  // the thread that read the sequence hands it over
+            if (tid == c.b) s_start->c = mine;
+            __syncthreads();
+            const int g = c.g;
+            c = s_start->c;
+            c.g = g;
+            if (c.tiles == 0) c.load(p);
+        } else {
+            c.load(p);
         }
-        base += chunk;
+        return c;
+    }
+    const long long all = sum * p.h_kv;
+    const int ctas = kv4_ctas(p, all);
+    if ((int)blockIdx.x >= ctas) return c;
+    lo = all * blockIdx.x / ctas;
+    hi = all * (blockIdx.x + 1) / ctas;
+    const long long want = lo / p.h_kv;  // (before b) <= want < (before b + 1)
+    if (p.batch <= NT) {
+        if (n > 0 && upto - n <= want && want < upto) {
+            s_start->c = mine;
+            s_start->before = upto - n;
+        }
+    } else {
+        long long base = 0;
+        for (int i0 = 0; i0 < p.batch && base <= want; i0 += NT) {
+            const int i = i0 + tid;
+            bool bad;
+            n = 0;
+            if (i < p.batch && kv4_sequence(p, i, mine.q0, mine.n_q, mine.kv_len, bad))
+                n = (mine.kv_len + p.tile - 1) / p.tile;
+            mine.b = i;
+            mine.tiles = n;
+            long long chunk;
+            const long long end = base + scan(n, chunk);
+            if (n > 0 && end - n <= want && want < end) {
+                s_start->c = mine;
+                s_start->before = end - n;
+            }
+            base += chunk;
+        }
     }
     __syncthreads();
-    c.b = s_start->b;
-    c.load(p);
+    c = s_start->c;
     const long long in = lo - s_start->before * p.h_kv;
     c.g = (int)(in / c.tiles);
     c.t = (int)(in % c.tiles);

@@ -1,23 +1,23 @@
 // Joins the partial results of units that several CTAs of a 4-bit attention call shared.
 //
 // One block per (unit, row): O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the unit's
-// partial slots, M their largest maximum.  The threads form 256 / D groups that take every
-// (256/D)-th slot and are added in group order, so the result does not depend on timing.  Bound
-// by load latency: a row's slots are read in parallel, a unit of one long sequence has up to
-// 2 x 148 of them.
+// partial slots, M their largest maximum.  The threads form NT / D groups that take every (NT/D)-th
+// slot and are added in group order, so the result does not depend on timing.  Bound by load
+// latency, so a thread's first eight outputs are loaded together with the statistics, before their
+// weights are known, and a unit of one long sequence, which up to 2 x 148 CTAs share, gets four
+// groups (1,024 bytes of a row in flight per slot and group).
 #include "kv4_common.cuh"
 
 namespace sd {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kMaxSlots = 1024;  // of one unit: at most the launch's CTAs, or its splits
+constexpr int kPre = 8;          // outputs of a thread loaded with the statistics
 
-template <typename T, int D>
+template <typename T, int D, int kThreads>
 __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const Kv4Params p) {
     pdl_trigger();  // (see launch_pdl)
     pdl_wait();
-    __shared__ long long s_red[2 * kThreads / 32];
     __shared__ float s_w[kMaxSlots];
     __shared__ float s_f[kThreads / 32];
     __shared__ float s_o[kThreads];
@@ -26,18 +26,13 @@ __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const Kv4Params p) 
     int q0, n_q, kv_len;
     bool bad;
     if (!kv4_sequence(p, b, q0, n_q, kv_len, bad) || lr >= n_q * p.group) return;
-    int64_t first, step;  // slots first, first + 1 * step ... (tensor cores: after the first one)
+    int64_t first, step;  // slots first, first + step, ... (tensor cores: after the first one)
     int n;
     if (p.ctas) {
-        long long total, before;
-        kv4_count<kThreads>(p, b, s_red, total, before);
-        total *= p.h_kv;
-        const int tiles = (kv_len + p.tile - 1) / p.tile;
-        const long long base = before * p.h_kv + (long long)g * tiles;
-        const int ctas = kv4_ctas(p, total), c0 = kv4_cta_of(base, total, ctas);
-        n = kv4_cta_of(base + tiles - 1, total, ctas) - c0 + 1;
+        const int2 c = __ldg(kv4_unit_ctas(p) + u);
+        n = c.y - c.x + 1;
         if (n == 1) return;  // the output is there already
-        first = 2 * (int64_t)c0;
+        first = 2 * (int64_t)c.x;
         step = 2;
     } else {
         n = p.n_splits;
@@ -45,6 +40,14 @@ __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const Kv4Params p) 
         step = 1;
     }
     auto slot = [&](int i) { return first + i * step + (p.ctas && i == 0 ? 1 : 0); };
+    constexpr int kGroups = kThreads / D;
+    const int col = tid % D, grp = tid / D;
+    float pre[kPre];
+#pragma unroll
+    for (int k = 0; k < kPre; ++k) {
+        const int i = grp + k * kGroups;
+        pre[k] = i < n ? kv4_slot_o(p, slot(i), lr)[col] : 0.f;
+    }
     float M = -INFINITY;
     for (int i = tid; i < n; i += kThreads) M = fmaxf(M, s_w[i] = kv4_slot_ml(p, slot(i), lr)[0]);
     M = warp_max(M);
@@ -66,11 +69,15 @@ __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const Kv4Params p) 
     L = 0.f;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) L += s_f[w];
-    constexpr int kGroups = kThreads / D;
-    const int col = tid % D, grp = tid / D;
     float acc = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPre; ++k) {
+        const int i = grp + k * kGroups;
+        if (i < n) acc = fmaf(s_w[i], pre[k], acc);
+    }
 #pragma unroll 8
-    for (int i = grp; i < n; i += kGroups) acc = fmaf(s_w[i], kv4_slot_o(p, slot(i), lr)[col], acc);
+    for (int i = grp + kPre * kGroups; i < n; i += kGroups)
+        acc = fmaf(s_w[i], kv4_slot_o(p, slot(i), lr)[col], acc);
     s_o[tid] = acc;
     __syncthreads();
     if (grp) return;
@@ -84,17 +91,22 @@ __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const Kv4Params p) 
         static_cast<unsigned short *>(p.out)[at] = (unsigned short)f32_to_bf16_bits(o);
 }
 
+template <typename T, int D>
+cudaError_t launch_d(const Kv4Params &p, cudaStream_t s) {
+    const dim3 grid(p.batch * p.h_kv, p.group * p.max_q_rows);
+    // slots that a unit has on average (two more where its ends are shared)
+    const int slots = p.ctas ? p.ctas / (p.batch * p.h_kv) : p.n_splits;
+    return slots > 8 ? launch_pdl(kv4_merge_kernel<T, D, 4 * D>, grid, dim3(4 * D), 0, s, p)
+                     : launch_pdl(kv4_merge_kernel<T, D, D>, grid, dim3(D), 0, s, p);
+}
+
 }  // namespace
 
 cudaError_t launch_kv4_merge(const Kv4Params &p, cudaStream_t s) {
-    const dim3 grid(p.batch * p.h_kv, p.group * p.max_q_rows);
     if (p.dtype == SD_BF16)
-        return p.head_dim == 128
-                   ? launch_pdl(kv4_merge_kernel<unsigned short, 128>, grid, dim3(kThreads), 0, s, p)
-                   : launch_pdl(kv4_merge_kernel<unsigned short, 64>, grid, dim3(kThreads), 0, s, p);
-    return p.head_dim == 128
-               ? launch_pdl(kv4_merge_kernel<float, 128>, grid, dim3(kThreads), 0, s, p)
-               : launch_pdl(kv4_merge_kernel<float, 64>, grid, dim3(kThreads), 0, s, p);
+        return p.head_dim == 128 ? launch_d<unsigned short, 128>(p, s)
+                                 : launch_d<unsigned short, 64>(p, s);
+    return p.head_dim == 128 ? launch_d<float, 128>(p, s) : launch_d<float, 64>(p, s);
 }
 
 }  // namespace sd

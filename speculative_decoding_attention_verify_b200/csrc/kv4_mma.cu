@@ -128,7 +128,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
     constexpr int kW = D / 32;  // 8-code words of a lane's share of a key
     constexpr bool kQRegs = NT == 1;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_red[2 * kThreads / 32];
+    __shared__ long long s_red[kThreads / 32];
     __shared__ Kv4Start s_start;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gq = lane >> 2, t4 = lane & 3;
@@ -552,6 +552,11 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
             }
             __syncthreads();
         }
+        if (tid == 0 && !p.whole) {
+            int *uc = reinterpret_cast<int *>(kv4_unit_ctas(p) + (int64_t)cc.b * p.h_kv + cc.g);
+            if (starts) uc[0] = blockIdx.x;
+            if (ends) uc[1] = blockIdx.x;
+        }
         if (slot == 0) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -618,7 +623,7 @@ cudaError_t launch_d(const Kv4Params &p, cudaStream_t s) {
 
 }  // namespace
 
-int kv4_mma_max_rows() { return 128; }
+int kv4_mma_max_rows() { return 16; }
 
 // Row blocks of 32 rows (1, 2 or 4 of them) leave 8, 4 or 2 slots of 32 positions to a tile.
 void kv4_mma_plan(int head_dim, int rows, int *tile, int *per_sm) {

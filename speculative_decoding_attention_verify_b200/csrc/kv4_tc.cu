@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     // (an offset from the array, so that accesses stay shared-memory instructions)
     uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
-    __shared__ long long s_red[2 * kThreads / 32];
+    __shared__ long long s_red[kThreads / 32];
     __shared__ Kv4Start s_start;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
@@ -771,6 +771,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                         ml[1] = l;
                     }
                 }
+            }
+            if (warp == 0 && lane == 0 && !p.whole) {
+                int *uc = reinterpret_cast<int *>(kv4_unit_ctas(p) + (int64_t)u.b * p.h_kv + u.g);
+                if (starts) uc[0] = blockIdx.x;
+                if (ends) uc[1] = blockIdx.x;
             }
             u = nx;
         }

@@ -5,21 +5,28 @@
 // q_out.  All of it is one pass over the rows, bound by their bytes (each read once and written
 // once) for a prompt and by launch and load latency for a decode step.
 //
-// A block takes 1 or 4 rows.  One warp per row finds the row's sequence (a 32-way search of
-// q_start, one round of loads for up to 32 sequences) and slot; the block then forms the row's
-// cosines and sines once for all heads: position * f_m is taken in turns and reduced to
-// [-1/2, 1/2] in fp64 (positions reach 1e6, where an fp32 angle is off by 0.06 rad), so the fp32
-// sine and cosine see a small argument.  A thread handles a unit of two VEC-element chunks of a
-// head, chosen so that both elements of every pair are its own (half layout: chunks rotary/2
-// apart), and so q_out may overwrite q.
+// append_kernel (16-byte aligned rows): a block of 8 warps takes 1 or 4 rows, 8 or 2 warps each.  A
+// thread handles a unit of two VEC-element chunks of a head, chosen so that both elements of every
+// pair are its own (half layout: chunks rotary/2 apart; q_out may so overwrite q), and goes with it
+// through the row's heads, loading two heads ahead.  It asks for the first ones at once, since
+// their place depends on nothing looked up.  Then its warp finds the row's sequence (a 32-way
+// search of q_start, one round of loads for up to 32 sequences) and slot, and the row's warps form
+// its cosines and sines, each once: position * f_m is taken in turns and reduced to [-1/2, 1/2] in
+// fp64 (positions reach 1e6, where an fp32 angle is off by 0.06 rad), so the fp32 sine and cosine
+// see a small argument.  A thread's own pairs' then stay in registers for all heads.
+// append_narrow_kernel takes the rest (odd strides and alignments, rotated parts that cut a
+// 16-byte chunk) one pair at a time.
 //
 // 4-bit rows: the D/(2 VEC) neighbouring lanes of a head share its minimum and maximum by
 // shuffles, and each writes its chunks' codes as one word per 8 channels.  A key's rotation is in
 // fp64 here: its rounded value decides codes, and a code is a whole step.  A code is the rounded
-// quotient (x - lo) / s: fp32 with one reciprocal per row, and in fp64 when the fp32 quotient is
-// within 1e-4 of a border (its own error is below 5e-6), which gives the fp64 quotient's code
-// every time at fp32 cost.
+// quotient (x - lo) / s: fp32 with one reciprocal per row, rounded by adding and subtracting
+// 1.5 2^23 (the sum's low bits are then the code), and in fp64 when the fp32 quotient is within
+// 1e-4 of a border (its own error is below 5e-6), which gives the fp64 quotient's code every time
+// at fp32 cost.
 #include <math.h>
+
+#include <cuda_bf16.h>
 
 #include "sd_internal.h"
 
@@ -50,27 +57,40 @@ __device__ __forceinline__ int find_sequence(const int32_t *q_start, int batch, 
 }
 
 template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f<unsigned short>(unsigned short x) {
-    return __uint_as_float((uint32_t)x << 16);
+__device__ __forceinline__ float to_f(T x) {
+    if constexpr (sizeof(T) == 4)
+        return x;
+    else
+        return __uint_as_float((uint32_t)x << 16);
 }
 template <typename T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ float from_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ unsigned short from_f<unsigned short>(float x) {
-    return (unsigned short)f32_to_bf16_bits(x);
+__device__ __forceinline__ T from_f(float x) {
+    if constexpr (sizeof(T) == 4)
+        return x;
+    else
+        return (T)f32_to_bf16_bits(x);
 }
 
-// VEC elements, moved as one 16-byte access when VEC > 1
+// 16 bytes of the rows' type as floats (8 for bf16, 4 for fp32), and back with one rounding.
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack {
-    T x[VEC];
-};
+__device__ __forceinline__ void unpack(const uint4 &w, float (&f)[VEC]) {
+    Chunk<sizeof(T) == 2>::to_float(w, f);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ uint4 pack(const float (&f)[VEC]) {
+    if constexpr (sizeof(T) == 4) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                          __float_as_uint(f[3]));
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
 
 __device__ __forceinline__ float bf16_round(float x) {
     return __uint_as_float(f32_to_bf16_bits(x) << 16);
@@ -90,174 +110,217 @@ __device__ __forceinline__ void row_params(float mn, float mx, bool bad, float &
     }
 }
 
+constexpr float kRoundMagic = 12582912.f;  // 1.5 2^23: adding it rounds to a whole number, ties to even
+
+// Code of x as a whole float; inv is 1 / s, or 0 for s == 0.
+template <typename T>
 __device__ __forceinline__ float code_of(float x, float s, float lo, float inv) {
-    if (!(s > 0.f)) return 0.f;
     const float q = (x - lo) * inv;
-    float c = rintf(q);
-    if (!(fabsf(q - c) < 0.4999f)) c = (float)rint(((double)x - (double)lo) / (double)s);
-    return fminf(fmaxf(c, 0.f), 15.f);
+    float c = (q + kRoundMagic) - kRoundMagic;
+    if (!(fabsf(q - c) < 0.4999f))
+        c = s > 0.f ? (float)rint(((double)x - (double)lo) / (double)s) : 0.f;
+    // (bf16 rows: lo is the minimum itself, and (max - lo) / s is below 15.04)
+    return sizeof(T) == 4 || !(c <= 15.f) ? fminf(fmaxf(c, 0.f), 15.f) : c;
 }
 
 __device__ __forceinline__ uint32_t param_bits(float s, float lo) {
     return (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
 }
 
+// Sequence, position and slot of row r (every lane of the warp gets them).
+__device__ __forceinline__ RowInfo find_row(const AppendParams &p, int r, int lane) {
+    RowInfo f{0, 0, 0, 0};
+    const int b = find_sequence(p.q_start, p.batch, r, lane);
+    if (b >= p.batch) return f;
+    const int q0 = __ldg(p.q_start + b), q1 = __ldg(p.q_start + b + 1), n = q1 - q0;
+    const int len = __ldg(p.kv_len + b);
+    if (q0 < 0 || q0 > r || r >= q1) return f;
+    if (q1 > p.n_rows || len < n || len > p.max_kv_len ||
+        (p.page_size && len > (int64_t)p.max_pages * kPageSize)) {
+        if (lane == 0) set_dev_err(p.dev_err, SD_DEVERR_SHAPE);
+        return f;
+    }
+    f.b = b;
+    f.j = len - n + (r - q0);
+    f.flags = 3;
+    if (p.page_size) {
+        f.page = __ldg(p.block_table + (int64_t)b * p.max_pages + (f.j >> 4));
+        if (f.page < 0 || f.page >= p.num_pages) {
+            if (lane == 0) set_dev_err(p.dev_err, SD_DEVERR_PAGE);
+            f.flags = 1;
+        }
+    }
+    return f;
+}
+
+// Position of row r, in turns of pair m, reduced to [-1/2, 1/2].
+__device__ __forceinline__ double turn_of(const AppendParams &p, const RowInfo &f, int r, int m) {
+    const int pos = p.pos ? __ldg(p.pos + r) : f.j;
+    const double t = (double)pos * p.rope.turns[m];
+    return t - rint(t);
+}
+
+__device__ __forceinline__ float2 cos_sin(const AppendParams &p, double t) {
+    float sn, cs;
+    sincospif((float)(2.0 * t), &sn, &cs);
+    const float g = (float)p.rope.gain;
+    return make_float2(g * cs, g * sn);
+}
+
+__device__ __forceinline__ double2 cos_sin_d(const AppendParams &p, double t) {
+    double sn, cs;
+    sincospi(2.0 * t, &sn, &cs);
+    return make_double2(p.rope.gain * cs, p.rope.gain * sn);
+}
+
+// Row number of head h at the row's slot (paged, and 4-bit caches), and its element offset.
+__device__ __forceinline__ int64_t slot_row(const AppendParams &p, const RowInfo &f, int h) {
+    return p.page_size ? ((int64_t)f.page * p.h_kv + h) * kPageSize + (f.j & 15)
+                       : (int64_t)f.b * p.stride_b + (int64_t)h * p.stride_h + f.j;
+}
+__device__ __forceinline__ int64_t slot_element(const AppendParams &p, const RowInfo &f, int h) {
+    return p.page_size ? slot_row(p, f, h) * p.head_dim
+                       : (int64_t)f.b * p.stride_b + (int64_t)h * p.stride_h +
+                             (int64_t)f.j * p.head_dim;
+}
+
 template <typename T, int D, int VEC, bool KV4>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 4)
+append_kernel(const __grid_constant__ AppendParams p) {
     pdl_trigger();  // (see launch_pdl)
     pdl_wait();
-    constexpr int UH = D / (2 * VEC);  // units of a head
-    using P = Pack<T, VEC>;
-    __shared__ RowInfo s_row[kMaxRows];
-    __shared__ float2 s_cs[kMaxRows][D / 2];
-    __shared__ double2 s_csd[KV4 ? kMaxRows : 1][KV4 ? D / 2 : 1];
-    __shared__ float s_val[(KV4 && VEC == 1) ? kThreads / 32 : 1][(KV4 && VEC == 1) ? D : 1];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int r0 = blockIdx.x * p.rows_per_block;
-    const int nr = min(p.rows_per_block, p.n_rows - r0);
-    if (warp < nr) {
-        const int r = r0 + warp;
-        const int b = find_sequence(p.q_start, p.batch, r, lane);
-        if (lane == 0) {
-            RowInfo f{0, 0, 0, 0};
-            if (b < p.batch) {
-                const int q0 = __ldg(p.q_start + b), q1 = __ldg(p.q_start + b + 1), n = q1 - q0;
-                const int len = __ldg(p.kv_len + b);
-                if (q0 >= 0 && q0 <= r && r < q1) {
-                    if (q1 > p.n_rows || len < n || len > p.max_kv_len ||
-                        (p.page_size && len > (int64_t)p.max_pages * kPageSize)) {
-                        set_dev_err(p.dev_err, SD_DEVERR_SHAPE);
-                    } else {
-                        f.b = b;
-                        f.j = len - n + (r - q0);
-                        f.flags = 3;
-                        if (p.page_size) {
-                            f.page = __ldg(p.block_table + (int64_t)b * p.max_pages + (f.j >> 4));
-                            if (f.page < 0 || f.page >= p.num_pages) {
-                                set_dev_err(p.dev_err, SD_DEVERR_PAGE);
-                                f.flags = 1;
-                            }
-                        }
-                    }
-                }
-            }
-            s_row[warp] = f;
-        }
-    }
-    __syncthreads();
+    constexpr int UH = D / (2 * VEC);  // units (lanes) of a head
+    // cosine and sine of pair u VEC + e at [e][u]
+    __shared__ float2 s_cs[kMaxRows][VEC][UH];
+    __shared__ double2 s_csd[KV4 ? kMaxRows : 1][KV4 ? VEC : 1][KV4 ? UH : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int wpr = kThreads / 32 / p.rows_per_block;  // warps of a row
+    const int row = warp / wpr, r = blockIdx.x * p.rows_per_block + row;
+    const bool here = r < p.n_rows;
+    const int slots = wpr * (32 / UH), slot = (warp % wpr) * (32 / UH) + lane / UH;
     const int rot = p.rope.rotary_dim, half_rot = rot >> 1;
-    for (int x = tid; x < nr * half_rot; x += kThreads) {
-        const int row = x / half_rot, m = x - row * half_rot;
-        const RowInfo f = s_row[row];
-        if (!(f.flags & 1)) continue;
-        const int pos = p.pos ? __ldg(p.pos + r0 + row) : f.j;
-        double t = (double)pos * p.rope.turns[m];
-        t -= rint(t);
-        if constexpr (KV4) {
-            double sn, cs;
-            sincospi(2.0 * t, &sn, &cs);
-            s_csd[row][m] = make_double2((double)p.rope.gain * cs, (double)p.rope.gain * sn);
-            s_cs[row][m] = make_float2((float)(p.rope.gain * cs), (float)(p.rope.gain * sn));
-        } else {
-            float sn, cs;
-            sincospif((float)(2.0 * t), &sn, &cs);
-            const float g = (float)p.rope.gain;
-            s_cs[row][m] = make_float2(g * cs, g * sn);
-        }
-    }
-    __syncthreads();
-
     const bool half = p.rope.layout == SD_ROPE_HALF;
-    const T *qin = static_cast<const T *>(p.q), *kin = static_cast<const T *>(p.k),
-            *vin = static_cast<const T *>(p.v);
-    // Channels of the two chunks of unit u: both elements of every pair of a rotated unit.
-    auto chunks = [&](int u, bool rotated, int &oa, int &ob) {
-        if (rotated && half) {
-            if (u * 2 * VEC < rot) {
-                oa = u * VEC;
-                ob = oa + half_rot;
+    const int u = lane % UH;  // this thread's unit of every head it handles
+    // Channels of the unit's two chunks in a head that is rotated, and in one that is copied.
+    const bool turns = u * 2 * VEC < rot;
+    const int ra = turns && half ? u * VEC : u * 2 * VEC;
+    const int rb = turns && half ? ra + half_rot : ra + VEC;
+    const int ca = u * 2 * VEC;
+
+    // heads: queries, keys, values (4-bit caches: queries here, the others below)
+    const int heads = p.h_q + (KV4 ? 0 : 2 * p.h_kv);
+    auto is_value = [&](int hd) { return hd >= p.h_q + p.h_kv; };
+    auto source = [&](int hd) {
+        return hd < p.h_q ? static_cast<const T *>(p.q) + (int64_t)r * p.q_stride + hd * D
+               : !is_value(hd)
+                   ? static_cast<const T *>(p.k) + (int64_t)r * p.k_stride + (hd - p.h_q) * D
+                   : static_cast<const T *>(p.v) + (int64_t)r * p.v_stride +
+                         (hd - p.h_q - p.h_kv) * D;
+    };
+    uint4 a0, b0, a1, b1;  // the next two heads' chunks
+    a0 = b0 = a1 = b1 = make_uint4(0u, 0u, 0u, 0u);
+    auto fetch = [&](uint4 &a, uint4 &b, int hd, int end) {
+        if (here && hd < end) {
+            const T *src = source(hd);
+            const bool v = is_value(hd);
+            a = *reinterpret_cast<const uint4 *>(src + (v ? ca : ra));
+            b = *reinterpret_cast<const uint4 *>(src + (v ? ca + VEC : rb));
+        }
+    };
+    fetch(a0, b0, slot, heads);
+    fetch(a1, b1, slot + slots, heads);
+
+    RowInfo f{0, 0, 0, 0};
+    if (here) f = find_row(p, r, lane);
+    if (f.flags & 1)
+        for (int m = (warp % wpr) * 32 + lane; m < half_rot; m += wpr * 32) {
+            const double t = turn_of(p, f, r, m);
+            if constexpr (KV4) {
+                const double2 cs = cos_sin_d(p, t);
+                s_csd[row][m % VEC][m / VEC] = cs;
+                s_cs[row][m % VEC][m / VEC] = make_float2((float)cs.x, (float)cs.y);
             } else {
-                oa = u * 2 * VEC;
-                ob = oa + VEC;
+                s_cs[row][m % VEC][m / VEC] = cos_sin(p, t);
             }
+        }
+    __syncthreads();
+    if (!(f.flags & 1)) return;
+    float2 cs[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) cs[e] = turns ? s_cs[row][e][u] : make_float2(1.f, 0.f);
+    // Turns the unit's pairs: g(index of the first and second element in a / b, e of the table).
+    auto pairs = [&](auto &&g) {
+        if (half) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) g(e, VEC + e, e);
         } else {
-            oa = u * 2 * VEC;
-            ob = oa + VEC;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (ra + 2 * e < rot) g(2 * e, 2 * e + 1, e);
         }
     };
-    // Pair m of unit u in a / b: element indexes through f(a, b, m)
-    auto turn = [&](int u, int oa, auto &&f) {
-        if (half || VEC == 1) {
-            if (u * 2 * VEC < rot)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) f(e, VEC + e, half ? oa + e : u);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 2 * VEC; e += 2)
-                if (oa + e < rot) f(e, e + 1, (oa + e) >> 1);
-        }
-    };
-    // heads handled by units: queries, then (dense caches, or wide chunks) keys and values
-    constexpr bool kKvUnits = !(KV4 && VEC == 1);
-    const int heads = p.h_q + (kKvUnits ? 2 * p.h_kv : 0);
-    const int per_row = heads * UH;
-    for (int x = tid; x < nr * per_row; x += kThreads) {
-        const int row = x / per_row, y = x - row * per_row;
-        const int hd = y / UH, u = y % UH;
-        const RowInfo f = s_row[row];
-        const int64_t r = r0 + row;
-        const bool is_q = hd < p.h_q, is_k = !is_q && hd < p.h_q + p.h_kv;
+#pragma unroll 1
+    for (int hd = slot; hd < heads; hd += slots) {
+        uint4 xa = a0, xb = b0;
+        a0 = a1;
+        b0 = b1;
+        fetch(a1, b1, hd + 2 * slots, heads);
+        const bool is_q = hd < p.h_q, is_v = is_value(hd);
         if (!(f.flags & (is_q ? 1 : 2))) continue;
-        const int h = is_q ? hd : is_k ? hd - p.h_q : hd - p.h_q - p.h_kv;
-        const T *src = is_q   ? qin + r * p.q_stride + (int64_t)h * D
-                       : is_k ? kin + r * p.k_stride + (int64_t)h * D
-                              : vin + r * p.v_stride + (int64_t)h * D;
-        int oa, ob;
-        chunks(u, is_q || is_k, oa, ob);
-        P ab[2];
-        ab[0] = *reinterpret_cast<const P *>(src + oa);
-        ab[1] = *reinterpret_cast<const P *>(src + ob);
-        auto at = [&](int e) -> T & { return ab[e / VEC].x[e % VEC]; };
-        if (is_q || (is_k && !KV4)) {
-            turn(u, oa, [&](int ea, int eb, int m) {
-                const float2 cs = s_cs[row][m];
-                const float a = to_f<T>(at(ea)), c = to_f<T>(at(eb));
-                at(ea) = from_f<T>(a * cs.x - c * cs.y);
-                at(eb) = from_f<T>(c * cs.x + a * cs.y);
+        if (turns && !is_v) {
+            float v[2][VEC];
+            unpack<T, VEC>(xa, v[0]);
+            unpack<T, VEC>(xb, v[1]);
+            pairs([&](int ea, int eb, int e) {
+                float &x = v[ea / VEC][ea % VEC], &y = v[eb / VEC][eb % VEC];
+                const float c = x, d = y;
+                x = c * cs[e].x - d * cs[e].y;
+                y = d * cs[e].x + c * cs[e].y;
             });
+            xa = pack<T, VEC>(v[0]);
+            xb = pack<T, VEC>(v[1]);
         }
-        if (is_q || !KV4) {
-            T *dst;
-            if (is_q) {
-                dst = static_cast<T *>(p.q_out) + (r * p.h_q + h) * D;
-            } else {
-                const int64_t o = p.page_size
-                                      ? (((int64_t)f.page * p.h_kv + h) * kPageSize + (f.j & 15)) * D
-                                      : (int64_t)f.b * p.stride_b + (int64_t)h * p.stride_h +
-                                            (int64_t)f.j * D;
-                dst = static_cast<T *>(is_k ? p.k_cache : p.v_cache) + o;
-            }
-            *reinterpret_cast<P *>(dst + oa) = ab[0];
-            *reinterpret_cast<P *>(dst + ob) = ab[1];
-        } else if constexpr (KV4 && VEC > 1) {
-            if (is_k) {
-                turn(u, oa, [&](int ea, int eb, int m) {
-                    const double2 cs = s_csd[row][m];
-                    const double a = to_f<T>(at(ea)), c = to_f<T>(at(eb));
-                    at(ea) = from_f<T>((float)(a * cs.x - c * cs.y));
-                    at(eb) = from_f<T>((float)(c * cs.x + a * cs.y));
+        T *dst = is_q   ? static_cast<T *>(p.q_out) + ((int64_t)r * p.h_q + hd) * D
+                 : is_v ? static_cast<T *>(p.v_cache) + slot_element(p, f, hd - p.h_q - p.h_kv)
+                        : static_cast<T *>(p.k_cache) + slot_element(p, f, hd - p.h_q);
+        *reinterpret_cast<uint4 *>(dst + (is_v ? ca : ra)) = xa;
+        *reinterpret_cast<uint4 *>(dst + (is_v ? ca + VEC : rb)) = xb;
+    }
+    if constexpr (KV4) {
+        if (!(f.flags & 2)) return;
+        const int end = p.h_q + 2 * p.h_kv;
+        fetch(a0, b0, p.h_q + slot, end);
+#pragma unroll 1
+        for (int hd = p.h_q + slot; hd < end; hd += slots) {
+            const bool is_k = !is_value(hd);
+            const int h = is_k ? hd - p.h_q : hd - p.h_q - p.h_kv;
+            const int oa = is_k ? ra : ca, ob = is_k ? rb : ca + VEC;
+            float v[2][VEC];
+            unpack<T, VEC>(a0, v[0]);
+            unpack<T, VEC>(b0, v[1]);
+            fetch(a0, b0, hd + slots, end);
+            if (is_k && turns) {
+                pairs([&](int ea, int eb, int e) {
+                    const double2 cd = s_csd[row][e][u];
+                    float &x = v[ea / VEC][ea % VEC], &y = v[eb / VEC][eb % VEC];
+                    const double c = x, d = y;
+                    x = (float)(c * cd.x - d * cd.y);
+                    y = (float)(d * cd.x + c * cd.y);
                 });
+                // (the key as the rows' type holds it)
+                unpack<T, VEC>(pack<T, VEC>(v[0]), v[0]);
+                unpack<T, VEC>(pack<T, VEC>(v[1]), v[1]);
             }
             float mn = INFINITY, mx = -INFINITY, zero = 0.f;
 #pragma unroll
             for (int e = 0; e < 2 * VEC; ++e) {
-                const float v = to_f<T>(at(e));
-                mn = fminf(mn, v);
-                mx = fmaxf(mx, v);
-                zero += v * 0.f;  // NaN once any element is not finite
+                const float w = v[e / VEC][e % VEC];
+                mn = fminf(mn, w);
+                mx = fmaxf(mx, w);
+                zero = fmaf(w, 0.f, zero);  // NaN once any element is not finite
             }
-            // the UH lanes of the head (aligned groups: every loop count is a multiple of UH)
-            const unsigned group = (UH == 32 ? 0xffffffffu : ((1u << UH) - 1u) << (lane & ~(UH - 1)));
+            // the UH lanes of the head (a head's lanes go through the loop together)
+            const unsigned group = UH == 32 ? 0xffffffffu : ((1u << UH) - 1u) << (lane & ~(UH - 1));
 #pragma unroll
             for (int o = UH / 2; o > 0; o >>= 1) {
                 mn = fminf(mn, __shfl_xor_sync(group, mn, o));
@@ -266,19 +329,34 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
             const bool bad = (__ballot_sync(group, zero != 0.f) & group) != 0u;
             float s, lo;
             row_params<T>(mn, mx, bad, s, lo);
-            const float inv = 1.f / s;
-            const int64_t rw = p.page_size ? ((int64_t)f.page * p.h_kv + h) * kPageSize + (f.j & 15)
-                                           : (int64_t)f.b * p.stride_b + (int64_t)h * p.stride_h + f.j;
+            const float inv = s > 0.f ? 1.f / s : 0.f;
+            // codes as whole floats; quotients near a border are taken again in fp64
+            float code[2][VEC], edge = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2 * VEC; ++e) {
+                const float q = (v[e / VEC][e % VEC] - lo) * inv;
+                const float c = (q + kRoundMagic) - kRoundMagic;
+                code[e / VEC][e % VEC] = c;
+                edge = fmaxf(edge, fabsf(q - c));
+                if (!(q < 16.f)) edge = 1.f;  // (also NaN)
+            }
+            if (!(edge < 0.4999f) || sizeof(T) == 4) {
+#pragma unroll
+                for (int e = 0; e < 2 * VEC; ++e)
+                    code[e / VEC][e % VEC] = code_of<T>(v[e / VEC][e % VEC], s, lo, inv);
+            }
+            const int64_t rw = slot_row(p, f, h);
             unsigned char *codes = static_cast<unsigned char *>(is_k ? p.k_cache : p.v_cache);
             T *vals = static_cast<T *>(is_k ? p.k_out : p.v_out);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                uint32_t w = 0;
+                // the sum of code_e 16^e from the floats' bits: each is the magic's plus the code
+                uint32_t w = 0u;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    const float k = code_of(to_f<T>(ab[c].x[e]), s, lo, inv);
-                    w |= (uint32_t)(int)k << (4 * e);
-                    ab[c].x[e] = from_f<T>(fmaf(s, k, lo));
+                    w += (__float_as_uint(code[c][e] + kRoundMagic) - __float_as_uint(kRoundMagic))
+                         << (4 * e);
+                    v[c][e] = fmaf(s, code[c][e], lo);
                 }
                 const int o = c ? ob : oa;
                 unsigned char *cp = codes + rw * (D / 2) + o / 2;
@@ -286,7 +364,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
                     *reinterpret_cast<uint32_t *>(cp) = w;
                 else
                     *reinterpret_cast<unsigned short *>(cp) = (unsigned short)w;
-                if (vals) *reinterpret_cast<P *>(vals + (r * p.h_kv + h) * D + o) = ab[c];
+                if (vals)
+                    *reinterpret_cast<uint4 *>(vals + ((int64_t)r * p.h_kv + h) * D + o) =
+                        pack<T, VEC>(v[c]);
             }
             if (u == 0) {
                 (is_k ? p.k_param : p.v_param)[rw] = param_bits(s, lo);
@@ -294,32 +374,94 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
             }
         }
     }
-    if constexpr (KV4 && VEC == 1) {
-        // Element-wise access: one warp per (row, K or V, head), the row's values through shared
-        // memory so that each lane holds neighbouring channels when it packs codes.
+}
+
+// One row per block, one pair of channels at a time.
+template <typename T, int D, bool KV4>
+__global__ void __launch_bounds__(kThreads) append_narrow_kernel(const __grid_constant__ AppendParams p) {
+    pdl_trigger();  // (see launch_pdl)
+    pdl_wait();
+    __shared__ float2 s_cs[D / 2];
+    __shared__ double2 s_csd[KV4 ? D / 2 : 1];
+    __shared__ float s_val[KV4 ? kThreads / 32 : 1][KV4 ? D : 1];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x;
+    const RowInfo f = find_row(p, r, lane);
+    if (!(f.flags & 1)) return;
+    const int rot = p.rope.rotary_dim, half_rot = rot >> 1;
+    const bool half = p.rope.layout == SD_ROPE_HALF;
+    if (tid < half_rot) {
+        const double t = turn_of(p, f, r, tid);
+        if constexpr (KV4) {
+            s_csd[tid] = cos_sin_d(p, t);
+            s_cs[tid] = make_float2((float)s_csd[tid].x, (float)s_csd[tid].y);
+        } else {
+            s_cs[tid] = cos_sin(p, t);
+        }
+    }
+    __syncthreads();
+    const T *kin = static_cast<const T *>(p.k) + (int64_t)r * p.k_stride;
+    const T *vin = static_cast<const T *>(p.v) + (int64_t)r * p.v_stride;
+    // channels of pair x of a head: rotated pairs first, then neighbours
+    auto channels = [&](int x, bool turned, int &a, int &b) {
+        a = turned && half ? x : 2 * x;
+        b = turned && half ? x + half_rot : a + 1;
+    };
+    for (int x = tid; x < p.h_q * (D / 2); x += kThreads) {
+        const int h = x / (D / 2), m = x % (D / 2);
+        const T *src = static_cast<const T *>(p.q) + (int64_t)r * p.q_stride + h * D;
+        T *dst = static_cast<T *>(p.q_out) + ((int64_t)r * p.h_q + h) * D;
+        int ia, ib;
+        channels(m, 2 * m < rot, ia, ib);
+        T a = src[ia], b = src[ib];
+        if (2 * m < rot) {
+            const float fa = to_f<T>(a), fb = to_f<T>(b);
+            a = from_f<T>(fa * s_cs[m].x - fb * s_cs[m].y);
+            b = from_f<T>(fb * s_cs[m].x + fa * s_cs[m].y);
+        }
+        dst[ia] = a;
+        dst[ib] = b;
+    }
+    if (!(f.flags & 2)) return;
+    if constexpr (!KV4) {
+        for (int x = tid; x < p.h_kv * (D / 2); x += kThreads) {
+            const int h = x / (D / 2), m = x % (D / 2);
+            const int64_t o = slot_element(p, f, h);
+            T *kd = static_cast<T *>(p.k_cache) + o, *vd = static_cast<T *>(p.v_cache) + o;
+            int ia, ib;
+            channels(m, 2 * m < rot, ia, ib);
+            T a = kin[h * D + ia], b = kin[h * D + ib];
+            if (2 * m < rot) {
+                const float fa = to_f<T>(a), fb = to_f<T>(b);
+                a = from_f<T>(fa * s_cs[m].x - fb * s_cs[m].y);
+                b = from_f<T>(fb * s_cs[m].x + fa * s_cs[m].y);
+            }
+            kd[ia] = a;
+            kd[ib] = b;
+            vd[2 * m] = vin[h * D + 2 * m];
+            vd[2 * m + 1] = vin[h * D + 2 * m + 1];
+        }
+    } else {
+        // One warp per (K or V, head), the row's values through shared memory so that each lane
+        // holds neighbouring channels when it packs codes.
         float *val = s_val[warp];
         constexpr int EL = D / 32;
-        for (int x = warp; x < nr * 2 * p.h_kv; x += kThreads / 32) {
-            const int row = x / (2 * p.h_kv), y = x - row * 2 * p.h_kv;
+        for (int y = warp; y < 2 * p.h_kv; y += kThreads / 32) {
             const bool is_k = y < p.h_kv;
             const int h = is_k ? y : y - p.h_kv;
-            const RowInfo f = s_row[row];
-            if (!(f.flags & 2)) continue;
-            const int64_t r = r0 + row;
-            const T *src = is_k ? kin + r * p.k_stride + (int64_t)h * D
-                                : vin + r * p.v_stride + (int64_t)h * D;
-            for (int u = lane; u < UH; u += 32) {
-                int oa, ob;
-                chunks(u, is_k, oa, ob);
-                float a = to_f<T>(src[oa]), c = to_f<T>(src[ob]);
-                if (is_k && 2 * u < rot) {
-                    const double2 cs = s_csd[row][u];
+            const T *src = (is_k ? kin : vin) + h * D;
+            for (int m = lane; m < D / 2; m += 32) {
+                const bool turned = is_k && 2 * m < rot;
+                int ia, ib;
+                channels(m, turned, ia, ib);
+                float a = to_f<T>(src[ia]), c = to_f<T>(src[ib]);
+                if (turned) {
+                    const double2 cs = s_csd[m];
                     const double da = a, dc = c;
                     a = to_f<T>(from_f<T>((float)(da * cs.x - dc * cs.y)));
                     c = to_f<T>(from_f<T>((float)(dc * cs.x + da * cs.y)));
                 }
-                val[oa] = a;
-                val[ob] = c;
+                val[ia] = a;
+                val[ib] = c;
             }
             __syncwarp();
             float v[EL], mn = INFINITY, mx = -INFINITY, zero = 0.f;
@@ -328,7 +470,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
                 v[e] = val[lane * EL + e];
                 mn = fminf(mn, v[e]);
                 mx = fmaxf(mx, v[e]);
-                zero += v[e] * 0.f;
+                zero = fmaf(v[e], 0.f, zero);
             }
             __syncwarp();  // (the buffer's next row)
 #pragma unroll
@@ -339,16 +481,15 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
             const bool bad = __any_sync(0xffffffffu, zero != 0.f);
             float s, lo;
             row_params<T>(mn, mx, bad, s, lo);
-            const float inv = 1.f / s;
-            const int64_t rw = p.page_size ? ((int64_t)f.page * p.h_kv + h) * kPageSize + (f.j & 15)
-                                           : (int64_t)f.b * p.stride_b + (int64_t)h * p.stride_h + f.j;
+            const float inv = s > 0.f ? 1.f / s : 0.f;
+            const int64_t rw = slot_row(p, f, h);
             uint32_t w = 0;
             T *vals = static_cast<T *>(is_k ? p.k_out : p.v_out);
 #pragma unroll
             for (int e = 0; e < EL; ++e) {
-                const float k = code_of(v[e], s, lo, inv);
+                const float k = code_of<T>(v[e], s, lo, inv);
                 w |= (uint32_t)(int)k << (4 * e);
-                if (vals) vals[(r * p.h_kv + h) * D + lane * EL + e] = from_f<T>(fmaf(s, k, lo));
+                if (vals) vals[((int64_t)r * p.h_kv + h) * D + lane * EL + e] = from_f<T>(fmaf(s, k, lo));
             }
             unsigned char *cp =
                 static_cast<unsigned char *>(is_k ? p.k_cache : p.v_cache) + rw * (D / 2) + lane * (EL / 2);
@@ -364,30 +505,33 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     }
 }
 
-template <typename T, int D, int VEC>
-cudaError_t launch_t(const AppendParams &p, cudaStream_t s) {
+template <typename T, int D, bool KV4>
+cudaError_t launch_t(const AppendParams &p, bool wide, cudaStream_t s) {
+    constexpr int VEC = 16 / (int)sizeof(T);
+    if (!wide)
+        return launch_pdl(append_narrow_kernel<T, D, KV4>, dim3(p.n_rows), dim3(kThreads), 0, s, p);
     const int blocks = (p.n_rows + p.rows_per_block - 1) / p.rows_per_block;
-    return p.kv4 ? launch_pdl(append_kernel<T, D, VEC, true>, dim3(blocks), dim3(kThreads), 0, s, p)
-                 : launch_pdl(append_kernel<T, D, VEC, false>, dim3(blocks), dim3(kThreads), 0, s, p);
+    return launch_pdl(append_kernel<T, D, VEC, KV4>, dim3(blocks), dim3(kThreads), 0, s, p);
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const AppendParams &p, bool wide, cudaStream_t s) {
+    return p.kv4 ? launch_t<T, D, true>(p, wide, s) : launch_t<T, D, false>(p, wide, s);
 }
 
 }  // namespace
 
 cudaError_t launch_append(AppendParams p, bool wide, cudaStream_t s) {
-    // one row per block while that leaves SMs free, else four (their cosines and sines then fill
-    // a block's threads once)
+    // one row per block while that leaves SMs free, else four (two warps then form a row's 64
+    // cosines and sines at once)
     p.rows_per_block = p.n_rows <= 2 * device_sm_count() ? 1 : kMaxRows;
     const bool bf = p.dtype == SD_BF16;
     // 16-byte chunks need both chunks of a rotated unit aligned
-    const int vec = bf ? 8 : 4;
-    if (p.rope.layout == SD_ROPE_HALF && p.rope.rotary_dim % (2 * vec) != 0) wide = false;
-    if (bf) {
-        if (p.head_dim == 128)
-            return wide ? launch_t<unsigned short, 128, 8>(p, s) : launch_t<unsigned short, 128, 1>(p, s);
-        return wide ? launch_t<unsigned short, 64, 8>(p, s) : launch_t<unsigned short, 64, 1>(p, s);
-    }
-    if (p.head_dim == 128) return wide ? launch_t<float, 128, 4>(p, s) : launch_t<float, 128, 1>(p, s);
-    return wide ? launch_t<float, 64, 4>(p, s) : launch_t<float, 64, 1>(p, s);
+    if (p.rope.layout == SD_ROPE_HALF && p.rope.rotary_dim % (bf ? 16 : 8) != 0) wide = false;
+    if (bf)
+        return p.head_dim == 128 ? launch_d<unsigned short, 128>(p, wide, s)
+                                 : launch_d<unsigned short, 64>(p, wide, s);
+    return p.head_dim == 128 ? launch_d<float, 128>(p, wide, s) : launch_d<float, 64>(p, wide, s);
 }
 
 }  // namespace sd

@@ -2,14 +2,19 @@
 // up to 16 rows (heads of the group x query rows), bf16.
 //
 // Mathematics.  A key is lo + s c with codes c = 0..15, so
-//     q . k = s (sum_e q_e (16 + c_e)) + (lo - 16 s) sum_e q_e
-// and the sum over channels is one bf16 product of the query with 16 + c, which a code becomes by
-// one shift and one and-or: bf16 16.0 has its four highest mantissa bits free, 0x4180 | c << 3.
-// No multiplication and no rounding (q and 16 + c are exact in bf16).  For the values
-//     sum_j p_j v_j = sum_j bf16(p_j s_j) (c_j - 8) + sum_j p_j (lo_j + 8 s_j)
-// with 16 + c - 24 = c - 8 exact too; V's scale is folded into the softmax weight, which is
-// rounded to bf16 for the product (a rounding that the bf16 cache's kernels make as well), and
-// codes are centred so that the weight's rounding acts on values no larger than v itself.
+//     q . k = s (sum_e q_e c_e) + lo (sum_e q_e)
+// and the sum over channels is one fp16 product of the query with the codes themselves: a code in
+// the low bits of an fp16 word IS the number c 2^-24 (a subnormal; the tensor cores take those
+// exactly), one in bits 4-7 is 16 c 2^-24.  So a pair of codes becomes an operand by one AND, after
+// one shift by 8 for every second byte, with no conversion, no rounding and no offset to take away
+// again.  The queries are scaled by a power of two per row (their largest to 2^13; bf16's 8 bits
+// fit fp16's 11, and an element has to be 2^-27 of the row's largest to lose any) and the odd
+// channels, whose codes sit in bits 4-7, by 1/16.  For the values
+//     sum_j p_j v_j = sum_j (p_j s_j) c_j + sum_j p_j lo_j
+// with w_j = p_j s_j taken as one exponential, w_j = 2^(x_j + log2 s_j - m), x_j the score in log2
+// units and m a running maximum of the whole exponent.  w is rounded to fp16 (2^-12 of itself, and
+// the largest w is between 1 and 2^14) and p = w / s is not rounded: it enters the sums of the
+// softmax and of p lo in fp32.  Rows of one value (s = 0, codes 0) count with s = 1 there.
 //
 // Layout.  Everything is transposed: S^T = K Q^T and O^T = V^T P^T by mma.sync m16n8k16 with 16
 // positions (S) or 16 channels (O) as M and 8 rows as N, because few rows would leave most of an
@@ -33,6 +38,8 @@
 // vote per 32 positions; a weight stays finite in bf16 far beyond that).
 // Query fragments are registers for NT = 1; for more they are read from shared memory, once for
 // both pages.
+#include <cuda_fp16.h>
+
 #include <type_traits>
 
 #include "kv4_common.cuh"
@@ -49,7 +56,10 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kPos = 32;       // positions of a warp per tile
 constexpr int kStages = 2;
-constexpr float kGrow = 16.0f;
+constexpr float kGrow = 14.0f;  // weights stay below fp16's largest number
+// A scale below this is taken for it: 1 / s stays in range, and codes of such rows are worth less
+// than 1e-26.
+constexpr float kMinScale = 8.0779357e-28f;  // 2^-90
 
 // CTAs per SM: registers of O^T decide.
 constexpr int ctas_per_sm(int nt) { return nt < 4 ? 2 : 1; }
@@ -80,27 +90,34 @@ __device__ __forceinline__ void cp_async4z(uint32_t dst, const void *src, int n)
                  : "memory");
 }
 
-// (x & 0x00780078) | 0x41804180: a pair of codes at bits 3..6 of both halves to bf16 16 + c
-__device__ __forceinline__ uint32_t code_pair(uint32_t x) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(0x00780078u), "r"(0x41804180u));
-    return r;
-}
-// codes at nibble p (0..3) of both halves of w
+// Codes at nibble P (0..3) of both halves of w as a pair of fp16 numbers: c 2^-24 (P even) or
+// 16 c 2^-24 (P odd).  w8 is w >> 8.
 template <int P>
-__device__ __forceinline__ uint32_t codes_at(uint32_t w) {
-    return code_pair(P == 0 ? w << 3 : w >> (P == 0 ? 0 : 4 * P - 3));
+__device__ __forceinline__ uint32_t codes_at(uint32_t w, uint32_t w8) {
+    return (P < 2 ? w : w8) & (P & 1 ? 0x00f000f0u : 0x000f000fu);
 }
-__device__ __forceinline__ uint32_t sub24(uint32_t x) {
-    const __nv_bfloat162 c = __floats2bfloat162_rn(24.f, 24.f);
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), c);
-    return *reinterpret_cast<const uint32_t *>(&r);
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -110,6 +127,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
+}
+
+// Power of two that brings a row's largest query element below 2^14, and 2^24 over it.
+__device__ __forceinline__ float query_scale(float top, float &unscale) {
+    const int e = (int)(__float_as_uint(top) >> 23);  // biased; 255: not finite
+    // (rows of zeros, and elements beyond 2^114 or not finite, keep a scale that is in range)
+    const int k = e == 0 || e == 255 ? 0 : min(max(127 + 13 - e, -100), 126);
+    unscale = __uint_as_float((uint32_t)(127 + 24 - k) << 23);
+    return __uint_as_float((uint32_t)(127 + k) << 23);
 }
 
 // m index of position r of a warp's 16: rows t, 4+t, 8+t, 12+t are m = 2t, 2t+1, 2t+8, 2t+9, so
@@ -230,7 +256,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
         // the last position that query row 0 sees: positions up to it need no mask
         const int first_limit = kv_len - cc.n_q;
         uint32_t qb[kQRegs ? kKs : 1][2];
-        float2 qs[NT];  // sums of the query channels of columns 2t, 2t + 1
+        float2 qs[NT], qe[NT];  // of columns 2t, 2t + 1: sums of the query, 2^24 / its scale
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = r_base + nt * 8 + gq;
@@ -239,12 +265,33 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                 static_cast<const unsigned short *>(p.q) +
                 ((int64_t)(cc.q0 + (has ? r / G : 0)) * p.h_q + cc.g * G + (has ? r % G : 0)) * D +
                 t4 * (D / 4));
-            float sum = 0.f;
+            uint4 x[kW];
+            float sum = 0.f, top = 0.f;
 #pragma unroll
             for (int w = 0; w < kW; ++w) {
-                const uint4 x = has ? __ldg(src + w) : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t f0 = __byte_perm(x.x, x.z, 0x5410), f1 = __byte_perm(x.x, x.z, 0x7632);
-                const uint32_t f2 = __byte_perm(x.y, x.w, 0x5410), f3 = __byte_perm(x.y, x.w, 0x7632);
+                x[w] = has ? __ldg(src + w) : make_uint4(0u, 0u, 0u, 0u);
+                float f[8];
+                Chunk<true>::to_float(x[w], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    sum += f[e];
+                    top = fmaxf(top, fabsf(f[e]));
+                }
+            }
+            sum += __shfl_xor_sync(FULL, sum, 1);
+            sum += __shfl_xor_sync(FULL, sum, 2);
+            top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
+            float unscale;
+            const float scale = query_scale(top, unscale);
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                float f[8];
+                Chunk<true>::to_float(x[w], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] *= e & 1 ? scale * 0.0625f : scale;
+                const uint32_t f0 = pack_f16(f[0], f[4]), f1 = pack_f16(f[1], f[5]);
+                const uint32_t f2 = pack_f16(f[2], f[6]), f3 = pack_f16(f[3], f[7]);
                 if constexpr (kQRegs) {
                     qb[2 * w][0] = f0;
                     qb[2 * w][1] = f1;
@@ -254,13 +301,10 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                     s_q[((2 * w) * NT + nt) * 32 + lane] = make_uint2(f0, f1);
                     s_q[((2 * w + 1) * NT + nt) * 32 + lane] = make_uint2(f2, f3);
                 }
-                sum += bf16_lo(x.x) + bf16_hi(x.x) + bf16_lo(x.y) + bf16_hi(x.y) + bf16_lo(x.z) +
-                       bf16_hi(x.z) + bf16_lo(x.w) + bf16_hi(x.w);
             }
-            sum += __shfl_xor_sync(FULL, sum, 1);
-            sum += __shfl_xor_sync(FULL, sum, 2);
-            qs[nt].x = __shfl_sync(FULL, sum, (2 * t4) * 4);
-            qs[nt].y = __shfl_sync(FULL, sum, (2 * t4 + 1) * 4);
+            qs[nt] = make_float2(__shfl_sync(FULL, sum, 8 * t4), __shfl_sync(FULL, sum, 8 * t4 + 4));
+            qe[nt] = make_float2(__shfl_sync(FULL, unscale, 8 * t4),
+                                 __shfl_sync(FULL, unscale, 8 * t4 + 4));
         }
         // (the merge's barriers at the end of a share keep the fragments until all have read them)
         if (!kQRegs) __syncthreads();
@@ -319,41 +363,48 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                     }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t x = kw[i][0][w], y = kw[i][1][w];
-                    const uint32_t a0 = codes_at<0>(x), a1 = codes_at<0>(y);
-                    const uint32_t a2 = codes_at<1>(x), a3 = codes_at<1>(y);
+                    const uint32_t x = kw[i][0][w], y = kw[i][1][w], x8 = x >> 8, y8 = y >> 8;
+                    const uint32_t a0 = codes_at<0>(x, x8), a1 = codes_at<0>(y, y8);
+                    const uint32_t a2 = codes_at<1>(x, x8), a3 = codes_at<1>(y, y8);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
                         mma16816(s[i][nt], a0, a1, a2, a3, f[0][nt].x, f[0][nt].y);
-                    const uint32_t b0 = codes_at<2>(x), b1 = codes_at<2>(y);
-                    const uint32_t b2 = codes_at<3>(x), b3 = codes_at<3>(y);
+                    const uint32_t b0 = codes_at<2>(x, x8), b1 = codes_at<2>(y, y8);
+                    const uint32_t b2 = codes_at<3>(x, x8), b3 = codes_at<3>(y, y8);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
                         mma16816(s[i][nt], b0, b1, b2, b3, f[1][nt].x, f[1][nt].y);
                 }
             }
-            // ---- exponents: scores in log2 units less the maximum ----
+            // ---- exponents of the weights: x + log2 s - m ----
             float2 nm[NT];  // (before a column's first visible position its maximum counts as 0)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 nm[nt] = make_float2(m[nt][0] == -INFINITY ? 0.f : -m[nt][0],
                                      m[nt][1] == -INFINITY ? 0.f : -m[nt][1]);
             bool grow = false;
+            float is[2][2], vl[2][2];  // 1 / s and lo / s of the values
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t *par =
                     reinterpret_cast<const uint32_t *>(st + i * C::kPageBytes + 2 * C::kPage);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t kp = par[gq + 8 * h];
+                    const uint32_t kp = par[gq + 8 * h], vp = par[16 + gq + 8 * h];
                     const float ks = param_scale(kp) * p.scale_log2;
-                    const float kl = fmaf(param_low(kp), p.scale_log2, -16.f * ks);
+                    const float kl = param_low(kp) * p.scale_log2;
+                    float sc = param_scale(vp);
+                    sc = sc == 0.f ? 1.f : fmaxf(sc, kMinScale);
+                    is[i][h] = rcp(sc);
+                    vl[i][h] = param_low(vp) * is[i][h];
+                    const float ls = lg2(sc);
                     const float2 ks2 = make_float2(ks, ks), kl2 = make_float2(kl, kl);
+                    const float2 ls2 = make_float2(ls, ls);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float2 x =
-                            __ffma2_rn(make_float2(s[i][nt][2 * h], s[i][nt][2 * h + 1]), ks2,
-                                       __ffma2_rn(kl2, qs[nt], nm[nt]));
+                        const float2 x = __ffma2_rn(
+                            __fmul2_rn(make_float2(s[i][nt][2 * h], s[i][nt][2 * h + 1]), qe[nt]), ks2,
+                            __ffma2_rn(kl2, qs[nt], __fadd2_rn(ls2, nm[nt])));
                         s[i][nt][2 * h] = x.x;
                         s[i][nt][2 * h + 1] = x.y;
                     }
@@ -415,26 +466,23 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint8_t *pg = st + i * C::kPageBytes;
-                const uint32_t *par = reinterpret_cast<const uint32_t *>(pg + 2 * C::kPage);
-                // ---- weights, and P^T in operand layout ----
+                // ---- weights, and their transpose in operand layout ----
                 uint32_t pt[NT][2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t vp = par[16 + gq + 8 * h];
-                    const float vs = param_scale(vp), vl = fmaf(8.f, vs, param_low(vp));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float a = s[i][nt][2 * h], b = s[i][nt][2 * h + 1];
-                        float2 vs2 = make_float2(vs, vs), vl2 = make_float2(vl, vl);
+                        float2 is2 = make_float2(is[i][h], is[i][h]);
+                        float2 vl2 = make_float2(vl[i][h], vl[i][h]);
                         if constexpr (kMasked) {  // a hidden position's NaN must not get through
-                            if (a == -INFINITY) vs2.x = vl2.x = 0.f;
-                            if (b == -INFINITY) vs2.y = vl2.y = 0.f;
+                            if (a == -INFINITY) is2.x = vl2.x = 0.f;
+                            if (b == -INFINITY) is2.y = vl2.y = 0.f;
                         }
-                        const float2 e = make_float2(ex2(a), ex2(b));
-                        l2[nt] = __fadd2_rn(l2[nt], e);
-                        cr2[nt] = __ffma2_rn(e, vl2, cr2[nt]);
-                        const float2 wv = __fmul2_rn(e, vs2);
-                        pt[nt][h] = transpose8(pack_bf16(wv.x, wv.y));
+                        const float2 w = make_float2(ex2(a), ex2(b));
+                        l2[nt] = __ffma2_rn(w, is2, l2[nt]);
+                        cr2[nt] = __ffma2_rn(w, vl2, cr2[nt]);
+                        pt[nt][h] = transpose8(pack_f16(w.x, w.y));
                     }
                 }
                 // ---- O^T += V^T P^T ----
@@ -460,13 +508,14 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t x = __byte_perm(vw[0][w], vw[1][w], h ? 0x7632 : 0x5410);
                         const uint32_t y = __byte_perm(vw[2][w], vw[3][w], h ? 0x7632 : 0x5410);
-                        const uint32_t a0 = sub24(codes_at<0>(x)), a1 = sub24(codes_at<1>(x));
-                        const uint32_t a2 = sub24(codes_at<0>(y)), a3 = sub24(codes_at<1>(y));
+                        const uint32_t x8 = x >> 8, y8 = y >> 8;
+                        const uint32_t a0 = codes_at<0>(x, x8), a1 = codes_at<1>(x, x8);
+                        const uint32_t a2 = codes_at<0>(y, y8), a3 = codes_at<1>(y, y8);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             mma16816(o[4 * w + 2 * h][nt], a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
-                        const uint32_t b0 = sub24(codes_at<2>(x)), b1 = sub24(codes_at<3>(x));
-                        const uint32_t b2 = sub24(codes_at<2>(y)), b3 = sub24(codes_at<3>(y));
+                        const uint32_t b0 = codes_at<2>(x, x8), b1 = codes_at<3>(x, x8);
+                        const uint32_t b2 = codes_at<2>(y, y8), b3 = codes_at<3>(y, y8);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             mma16816(o[4 * w + 2 * h + 1][nt], b0, b1, b2, b3, pt[nt][0], pt[nt][1]);
@@ -568,8 +617,9 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                     float x[D / 8];
 #pragma unroll
                     for (int mt = 0; mt < kKs; ++mt) {
-                        x[2 * mt] = o[mt][nt][c] + cr[nt][c];
-                        x[2 * mt + 1] = o[mt][nt][2 + c] + cr[nt][c];
+                        // (codes of odd channels were 16 times as large)
+                        x[2 * mt] = fmaf(o[mt][nt][c], 16777216.f, cr[nt][c]);
+                        x[2 * mt + 1] = fmaf(o[mt][nt][2 + c], 1048576.f, cr[nt][c]);
                     }
                     if (starts && ends) {
                         const float inv = l[nt][c] == 0.f ? 0.f : 1.f / l[nt][c];

@@ -11,6 +11,8 @@
 // share the units instead, each a range of whole ones: nothing is left to join.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "sd_internal.h"
 
 namespace sd {
@@ -47,6 +49,54 @@ __device__ __forceinline__ float param_low(uint32_t w) { return __uint_as_float(
 // CTAs that take part: no more than there are tiles, so that each has one at least.
 __device__ __forceinline__ int kv4_ctas(const Kv4Params &p, long long total) {
     return (int)(total < p.ctas ? total : p.ctas);
+}
+
+// ---- what the tensor-core kernels share of the mathematics (kv4_mma.cu) ----
+
+__device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4z(uint32_t dst, const void *src, int n) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+}
+
+// A scale below this is taken for it: 1 / s stays in range, and codes of such rows are worth less
+// than 1e-26.
+constexpr float kMinScale = 8.0779357e-28f;  // 2^-90
+
+// Codes at nibble P (0..3) of both halves of w as a pair of fp16 numbers: c 2^-24 (P even) or
+// 16 c 2^-24 (P odd).  w8 is w >> 8.
+template <int P>
+__device__ __forceinline__ uint32_t codes_at(uint32_t w, uint32_t w8) {
+    return (P < 2 ? w : w8) & (P & 1 ? 0x00f000f0u : 0x000f000fu);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Power of two that brings a row's largest query element below 2^14, and 2^24 over it.
+__device__ __forceinline__ float query_scale(float top, float &unscale) {
+    const int e = (int)(__float_as_uint(top) >> 23);  // biased; 255: not finite
+    // (rows of zeros, and elements beyond 2^114 or not finite, keep a scale that is in range)
+    const int k = e == 0 || e == 255 ? 0 : min(max(127 + 13 - e, -100), 126);
+    unscale = __uint_as_float((uint32_t)(127 + 24 - k) << 23);
+    return __uint_as_float((uint32_t)(127 + k) << 23);
 }
 
 // The CTAs that hold a unit's first and last tile, written by those CTAs for the merge.

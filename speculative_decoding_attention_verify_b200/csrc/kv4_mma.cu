@@ -38,8 +38,6 @@
 // vote per 32 positions; a weight stays finite in bf16 far beyond that).
 // Query fragments are registers for NT = 1; for more they are read from shared memory, once for
 // both pages.
-#include <cuda_fp16.h>
-
 #include <type_traits>
 
 #include "kv4_common.cuh"
@@ -57,9 +55,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kPos = 32;       // positions of a warp per tile
 constexpr int kStages = 2;
 constexpr float kGrow = 14.0f;  // weights stay below fp16's largest number
-// A scale below this is taken for it: 1 / s stays in range, and codes of such rows are worth less
-// than 1e-26.
-constexpr float kMinScale = 8.0779357e-28f;  // 2^-90
 
 // CTAs per SM: registers of O^T decide.
 constexpr int ctas_per_sm(int nt) { return nt < 4 ? 2 : 1; }
@@ -81,39 +76,6 @@ struct MmaCfg {
 static_assert(2 * (MmaCfg<128, 2>::kSmem + 1024) <= 227 * 1024, "two CTAs per SM");
 static_assert(MmaCfg<128, 4>::kSmem <= 226 * 1024, "shared memory");
 
-__device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, int n) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async4z(uint32_t dst, const void *src, int n) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
-                 : "memory");
-}
-
-// Codes at nibble P (0..3) of both halves of w as a pair of fp16 numbers: c 2^-24 (P even) or
-// 16 c 2^-24 (P odd).  w8 is w >> 8.
-template <int P>
-__device__ __forceinline__ uint32_t codes_at(uint32_t w, uint32_t w8) {
-    return (P < 2 ? w : w8) & (P & 1 ? 0x00f000f0u : 0x000f000fu);
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 p = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&p);
-}
-
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -127,15 +89,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
-}
-
-// Power of two that brings a row's largest query element below 2^14, and 2^24 over it.
-__device__ __forceinline__ float query_scale(float top, float &unscale) {
-    const int e = (int)(__float_as_uint(top) >> 23);  // biased; 255: not finite
-    // (rows of zeros, and elements beyond 2^114 or not finite, keep a scale that is in range)
-    const int k = e == 0 || e == 255 ? 0 : min(max(127 + 13 - e, -100), 126);
-    unscale = __uint_as_float((uint32_t)(127 + 24 - k) << 23);
-    return __uint_as_float((uint32_t)(127 + k) << 23);
 }
 
 // m index of position r of a warp's 16: rows t, 4+t, 8+t, 12+t are m = 2t, 2t+1, 2t+8, 2t+9, so
@@ -193,6 +146,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
     };
     look_up();
     int copied = 0;
+    int64_t unit_row = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h;  // (contiguous)
     auto copy_next = [&]() {
         if (copied < n_my) {
             const int j0 = pc.t * p.tile + slot * kPos;
@@ -201,7 +155,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                 const int j = j0 + i * kPageSize;
                 int n = pc.kv_len - j;  // positions of this page
                 if (n > 0) {
-                    int64_t row0 = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h + j;
+                    int64_t row0 = unit_row + j;
                     if (p.page_size) {
                         row0 = ((int64_t)pages[i] * p.h_kv + pc.g) * kPageSize;
                         if (pages[i] < 0 || pages[i] >= p.num_pages) {
@@ -237,6 +191,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
             }
             ++copied;
             pc.next(p);
+            if (pc.t == 0) unit_row = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h;
             if (copied < n_my) look_up();
         }
         cp_async_commit();

@@ -1,28 +1,27 @@
 // tcgen05 attention over a 4-bit cache for many rows per KV head (verification): 17 to 128 rows,
 // bf16.
 //
-// The mathematics is kv4_mma.cu's: scores are products of q with 16 + c, corrected per position
-// by the row's s and lo; V enters as c - 8 with its scale folded into the softmax weights.  With
-// this many rows the products outgrow mma.sync (1,024 products per cycle per SM; a tile of 64 rows
-// would need 2,048 cycles, three times what it takes from HBM), so the codes are expanded to bf16
-// tiles in shared memory once and used by tcgen05.mma (4,096 products per cycle).
+// The mathematics is kv4_mma.cu's: codes are fp16 numbers as they stand, the queries are scaled
+// per row, and V's scale is in the weights' exponent.  With this many rows the products outgrow
+// mma.sync (1,024 products per cycle per SM; a tile of 64 rows would need 2,048 cycles, three times
+// what it takes from HBM), so the codes are spread to fp16 tiles in shared memory once and used by
+// tcgen05.mma (4,096 products per cycle).
 //
 // One persistent CTA per SM, 14 warps; the CTAs share all units' tiles evenly (kv4_common.cuh).
 //   warps 0-3  softmax: TMEM lane r holds MMA row r.  The unit's R rows are placed NCP times
 //              (4 copies up to 32 rows, 2 up to 64, else 1) and each warp handles 128 / NCP
 //              columns of its copy, so a tile's exponentials are spread over all four warps
 //   warps 4-11 expand: each streams 16 positions of every tile (a page) through its own ring of
-//              cp.async stages and writes them as bf16 into the K and V tiles (128-byte rows of
-//              64 channels, 128-byte swizzle), with the positions' four factors beside them
+//              cp.async stages and writes them as fp16 into the K and V tiles (128-byte rows of
+//              64 channels, 128-byte swizzle), with the positions' five factors beside them
 //   warp 12    S = Q K^T issuer (Q from TMEM), TMEM owner
 //   warp 13    O += P V issuer (P from TMEM)
-// A word of 8 codes becomes one 16-byte chunk by 4 shifts and 4 and-ors, its channels in the order
+// A word of 8 codes becomes one 16-byte chunk by 4 ANDs and a shift, its channels in the order
 // 0 4 1 5 2 6 3 7; Q is written to TMEM in the same order and O's columns are read back in it, so
 // no code is ever moved to its own place.
 // The softmax takes 32 columns at a time in one pass: the exponents are taken from the running
-// maximum as it stands, and only when one exceeds it by more than 2^16 does the maximum move
-// (then O, the sums and the tile's earlier weights are rescaled; weights stay finite in bf16 far
-// beyond that).  A second pass, or a tile's columns unrolled into one block of code, costs more
+// maximum as it stands, and only when one exceeds it by more than 2^14 does the maximum move
+// (then O, the sums and the tile's earlier weights are rescaled).  A second pass, or a tile's columns unrolled into one block of code, costs more
 // than its instructions: the warps' roles together must stay within the instruction cache (with
 // 64 columns and 32 positions unrolled, two of three issue slots were lost to instruction fetch
 // and a tile took 7,000 cycles).
@@ -53,9 +52,11 @@ constexpr int kStages = 4;           // cp.async ring of an expanding warp
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;      // S / P buffers at 0 and 128
 constexpr uint32_t kColQ = 384;
-constexpr float kRescaleLog2 = 16.0f;
+constexpr float kRescaleLog2 = 14.0f;  // weights stay below fp16's largest number
 constexpr uint32_t kHalfBytes = kTile * 128;  // 64 channels of a tile
-constexpr int kParSlots = 4;         // tiles whose position factors are kept
+constexpr int kParSlots = 4;         // tiles whose position factors are kept:
+// pairs of positions' (s, lo) of K [0, 256), log2 s of V [256, 384), (1 / s, lo / s) [384, 640)
+constexpr int kParFloats = 5 * kTile;
 
 template <int D>
 struct TcCfg {
@@ -65,7 +66,7 @@ struct TcCfg {
     static constexpr int kStageBytes = 2 * kCodes + 128;   // with its parameters
     static constexpr int kRing = 4 * kTileBytes;           // after K0 K1 V0 V1
     static constexpr int kPar = kRing + kExpandWarps * kStages * kStageBytes;
-    static constexpr int kScratch = kPar + kParSlots * 4 * kTile * 4;
+    static constexpr int kScratch = kPar + kParSlots * kParFloats * 4;
     // maxima and sums of every MMA row, then 32 columns of the copies' outputs
     static constexpr int kScratchBytes = (2 * kRows + 96 * 32) * 4;
     static constexpr int kBars = kScratch + kScratchBytes;
@@ -73,27 +74,10 @@ struct TcCfg {
 };
 static_assert(TcCfg<128>::kSmem <= 227 * 1024, "shared memory");
 
-__device__ __forceinline__ uint32_t pair_at(uint32_t w, int p) {
-    uint32_t x = p == 0 ? w << 3 : w >> (4 * p - 3), r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(0x00780078u), "r"(0x41804180u));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t sub24(uint32_t x) {
-    const __nv_bfloat162 c = __floats2bfloat162_rn(24.f, 24.f);
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), c);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
-__device__ __forceinline__ void copy16z(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(in ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy4z(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-                 "r"(in ? 4 : 0)
-                 : "memory");
+// kind::f16 instruction descriptor: fp32 accumulate, fp16 A and B, M = 128.
+__host__ __device__ constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
+    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(128 >> 4) << 24);
 }
 
 // 16 consecutive columns of this thread's TMEM lane.  Stores are not waited for: a wait::st comes
@@ -272,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                        : 0;
         };
         look_up();
+        int64_t unit_row = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h;  // (contiguous)
         constexpr int Q = C::kRow / 16;  // 16-byte chunks of a row
         // chunk q of row r is kept at q ^ (r / (8 / Q) mod Q): 8 rows' chunks in different banks
         auto raw_at = [](int r, int q) { return r * C::kRow + ((q ^ ((r / (8 / Q)) % Q)) << 4); };
@@ -280,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                 const uint32_t dst = ring + (copied % kStages) * C::kStageBytes;
                 const int j = pc.t * kTile + ew * kPageSize;
                 int n = pc.kv_len - j;  // positions (rows past the end are zeros)
-                int64_t row0 = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h + j;
+                int64_t row0 = unit_row + j;
                 if (p.page_size) {
                     row0 = ((int64_t)page * p.h_kv + pc.g) * kPageSize;
                     if (n > 0 && (page < 0 || page >= p.num_pages)) {
@@ -294,15 +279,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                     const int x = lane + 32 * k, r = x / Q, q = x % Q;
                     const bool in = r < n;
                     const int64_t off = (row0 + (in ? r : 0)) * C::kRow + q * 16;
-                    copy16z(dst + raw_at(r, q), p.k + off, in);
-                    copy16z(dst + C::kCodes + raw_at(r, q), p.v + off, in);
+                    cp_async16z(dst + raw_at(r, q), p.k + off, in ? 16 : 0);
+                    cp_async16z(dst + C::kCodes + raw_at(r, q), p.v + off, in ? 16 : 0);
                 }
                 const int r = lane & 15;
                 const bool in = r < n;
-                copy4z(dst + 2 * C::kCodes + lane * 4,
-                       (lane < 16 ? p.kp : p.vp) + row0 + (in ? r : 0), in);
+                cp_async4z(dst + 2 * C::kCodes + lane * 4,
+                       (lane < 16 ? p.kp : p.vp) + row0 + (in ? r : 0), in ? 4 : 0);
                 ++copied;
                 pc.next(p);
+                if (pc.t == 0) unit_row = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h;
                 if (copied < n_my) look_up();
             }
             cp_async_commit();
@@ -310,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) copy_next();
         // lane: row (lane & 15), chunks (lane >> 4), (lane >> 4) + 2
-        auto expand = [&](const uint8_t *src, uint8_t *dst, auto &&f) {
+        auto expand = [&](const uint8_t *src, uint8_t *dst) {
             const int r = lane & 15;
             // word c of chunk q is 16-byte chunk 4 (q & 1) + c of the row in half q / 2
             const uint32_t at = (uint32_t)((ew * kPageSize + r) * 128) |
@@ -320,10 +306,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                 const uint4 x = *reinterpret_cast<const uint4 *>(src + raw_at(r, 2 * k + (lane >> 4)));
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t w8 = w[c] >> 8;
                     *reinterpret_cast<uint4 *>(dst + k * kHalfBytes + (at ^ (uint32_t)(c << 4))) =
-                        make_uint4(f(pair_at(w[c], 0)), f(pair_at(w[c], 1)), f(pair_at(w[c], 2)),
-                                   f(pair_at(w[c], 3)));
+                        make_uint4(codes_at<0>(w[c], w8), codes_at<1>(w[c], w8),
+                                   codes_at<2>(w[c], w8), codes_at<3>(w[c], w8));
+                }
             }
             fence_async_smem();
             __syncwarp();
@@ -342,24 +330,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                 const uint32_t *par = reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes);
                 // (lanes 0-15 the key's two, lanes 16-31 the value's)
                 const uint32_t w = par[lane];
-                // per pair of positions: two scales, two offsets
-                float *d = s_par + (t % kParSlots) * 4 * kTile + (lane >> 4) * 2 * kTile +
-                           (ew * (kPageSize / 2) + ((lane & 15) >> 1)) * 4 + (lane & 1);
-                const float sc = param_scale(w), lw = param_low(w);
-                const float a = lane < 16 ? sc * p.scale_log2 : sc;
-                d[0] = a;
-                d[2] = lane < 16 ? fmaf(lw, p.scale_log2, -16.f * a) : fmaf(8.f, a, lw);
+                const float lw = param_low(w);
+                float sc = param_scale(w);
+                const int j = ew * kPageSize + (lane & 15);
+                float *d = s_par + (t % kParSlots) * kParFloats + (j >> 1) * 4 + (j & 1);
+                if (lane < 16) {
+                    d[0] = sc * p.scale_log2;
+                    d[2] = lw * p.scale_log2;
+                } else {
+                    sc = sc == 0.f ? 1.f : fmaxf(sc, kMinScale);
+                    const float inv = rcp(sc);
+                    s_par[(t % kParSlots) * kParFloats + 2 * kTile + j] = lg2(sc);
+                    d[3 * kTile] = inv;
+                    d[3 * kTile + 2] = lw * inv;
+                }
             }
-            expand(st, sK + s * C::kTileBytes, [](uint32_t x) { return x; });
+            expand(st, sK + s * C::kTileBytes);
             if (lane == 0) mbar_arrive(BAR(KF + s));
             if (t >= 2 && !wait1(PD + s, (t - 2) >> 1)) break;
-            expand(st + C::kCodes, sV + s * C::kTileBytes, [](uint32_t x) { return sub24(x); });
+            expand(st + C::kCodes, sV + s * C::kTileBytes);
             if (lane == 0) mbar_arrive(BAR(VF + s));
         }
         cp_async_wait<0>();
     } else if (warp == kSWarp) {
         // ---------------------------------------------------------- S = Q K^T issuer ---------
-        const uint32_t idesc = idesc_bf16(kTile, false);
+        const uint32_t idesc = idesc_f16(kTile, false);
         bool issued = false;
         Kv4Cursor c = first;
         int seg = 0;
@@ -372,12 +367,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             if (!ok) break;
             tc_after();
             if (lane == 0) {
-                const uint32_t kb = saddr(sK + s * C::kTileBytes);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ts(tmem + s * kTile, tmem + kColQ + kk * 8,
-                           desc_k_sw128(kb + (kk >> 2) * kHalfBytes + (kk & 3) * 32), idesc,
-                           kk > 0 ? 1u : 0u);
+                uint32_t kb = saddr(sK + s * C::kTileBytes);
+#pragma unroll 1
+                for (int h = 0; h < D / 64; ++h, kb += kHalfBytes)
+#pragma unroll 1
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ts(tmem + s * kTile, tmem + kColQ + (h * 4 + kk) * 8,
+                               desc_k_sw128(kb + kk * 32), idesc, h + kk > 0 ? 1u : 0u);
                 mma_commit(BAR(SF + s));
                 mma_commit(BAR(KE + s));
                 mbar_arrive(BAR(SF + s));  // (orders the factors before the softmax's reads)
@@ -396,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
         __syncwarp();
     } else if (warp == kPvWarp) {
         // ---------------------------------------------------------- O += P V issuer ----------
-        const uint32_t idesc = idesc_bf16(D, true);
+        const uint32_t idesc = idesc_f16(D, true);
         bool issued = false;
         Kv4Cursor c = first;
         for (int t = 0; t < n_my; ++t) {
@@ -407,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             const bool last = t + 1 == n_my || c.t + 1 == c.tiles;
             if (lane == 0) {
                 const uint32_t vb = saddr(sV + s * C::kTileBytes);
-#pragma unroll
+#pragma unroll 1
                 for (int kk = 0; kk < kTile / 16; ++kk)
                     mma_ts(tmem + kColO, tmem + s * kTile + kk * 8,
                            desc_mn_sw128(vb + kk * 2048, kHalfBytes), idesc,
@@ -438,34 +434,49 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
         float *s_m = reinterpret_cast<float *>(smem + C::kScratch), *s_l = s_m + kRows;
         float4 *s_o = reinterpret_cast<float4 *>(s_l + kRows);  // [copy - 1][RPC][8]
         // Q of unit u into TMEM (zeros past its rows), channels of each group of 8 in the order of
-        // the expanded codes; returns the row's sum.
+        // the spread codes.
+        float qsum, unscale;  // of this lane's row: sum of the query, 2^24 / its scale
         auto write_q = [&](const Kv4Cursor &u) {
             const bool has = r < u.n_q * G;
             const uint4 *src = reinterpret_cast<const uint4 *>(
                 static_cast<const unsigned short *>(p.q) +
                 ((int64_t)(u.q0 + (has ? r / G : 0)) * p.h_q + u.g * G + (has ? r % G : 0)) * D);
-            float sum = 0.f;
+            auto load = [&](int c, float (&f)[8]) {
+                Chunk<true>::to_float(has ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u), f);
+            };
+            float top = 0.f;
+            qsum = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < D / 8; ++c) {
+                float f[8];
+                load(c, f);
 #pragma unroll
-            for (int hh = 0; hh < D / 64; ++hh) {
-                float qf[32];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint4 x = has ? __ldg(src + hh * 8 + c) : make_uint4(0u, 0u, 0u, 0u);
-                    qf[4 * c] = __uint_as_float(__byte_perm(x.x, x.z, 0x5410));
-                    qf[4 * c + 1] = __uint_as_float(__byte_perm(x.x, x.z, 0x7632));
-                    qf[4 * c + 2] = __uint_as_float(__byte_perm(x.y, x.w, 0x5410));
-                    qf[4 * c + 3] = __uint_as_float(__byte_perm(x.y, x.w, 0x7632));
-                    sum += (bf16_lo(x.x) + bf16_hi(x.x)) + (bf16_lo(x.y) + bf16_hi(x.y)) +
-                           ((bf16_lo(x.z) + bf16_hi(x.z)) + (bf16_lo(x.w) + bf16_hi(x.w)));
+                for (int e = 0; e < 8; ++e) {
+                    qsum += f[e];
+                    top = fmaxf(top, fabsf(f[e]));
                 }
-                tmem_st32(lane_base + kColQ + hh * 32, qf);
             }
+            const float scale = query_scale(top, unscale);
+#pragma unroll 1
+            for (int c = 0; c < D / 8; c += 4) {
+                uint32_t q[16];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float f[8];
+                    load(c + i, f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] *= e & 1 ? scale * 0.0625f : scale;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) q[4 * i + e] = pack_f16(f[e], f[e + 4]);
+                }
+                tmem_st16(lane_base + kColQ + c * 4, q);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_before();
             mbar_arrive(BAR(QF));
-            return sum;
         };
         Kv4Cursor u = first;
-        float qsum = write_q(u);
+        write_q(u);
         bool ok_run = true;
         int t = 0, seg = 0;
         // The softmax itself works on fragments: lane (g, t4) has rows g + 8 k (k = 0..3) of the
@@ -479,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             const bool row_ok = r < R;
             const int first_limit = u.kv_len - u.n_q;
             const int seg_lo = u.t;
-            float mk[4], nm[4], qs[4];
+            float mk[4], nm[4], qs[4], qe[4];
             int limit[4];  // last visible position (rows past R see nothing)
             float2 l2[4], cr2[4];
 #pragma unroll
@@ -488,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                 mk[k] = -INFINITY;
                 nm[k] = 0.f;
                 qs[k] = __shfl_sync(FULL, qsum, gq + 8 * k);
+                qe[k] = __shfl_sync(FULL, unscale, gq + 8 * k);
                 limit[k] = rk < R ? first_limit + rk / G : -1;
                 l2[k] = cr2[k] = make_float2(0.f, 0.f);
             }
@@ -510,8 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                 }
                 tc_after();
                 const uint32_t s_addr = lane_base + s * kTile;
-                const float4 *par =
-                    reinterpret_cast<const float4 *>(s_par + (t % kParSlots) * 4 * kTile) + t4;
+                const float *par = s_par + (t % kParSlots) * kParFloats;
                 const int p0 = lt * kTile;
                 // every row sees every position of the tile (rows past R may compute anything)
                 const bool interior = p0 + kTile - 1 <= first_limit;
@@ -521,18 +532,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                     const int cb = c0 + ch * 32;
                     float v[2][16];
                     tmem_ld_frag(s_addr + cb, v);
-                    // exponents of the weights: the scores in log2 units less the maximum
+                    // exponents of the weights: x + log2 s - m
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float4 f = par[cb / 2 + 4 * i];
+                        const int at = cb / 2 + 4 * i + t4;  // the pair of positions
+                        const float4 f = reinterpret_cast<const float4 *>(par)[at];
+                        const float2 ls = reinterpret_cast<const float2 *>(par + 2 * kTile)[at];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             float &a = v[k >> 1][4 * i + 2 * (k & 1)];
                             float &b = v[k >> 1][4 * i + 2 * (k & 1) + 1];
                             const float2 x = __ffma2_rn(
-                                make_float2(a, b), make_float2(f.x, f.y),
+                                __fmul2_rn(make_float2(a, b), make_float2(qe[k], qe[k])),
+                                make_float2(f.x, f.y),
                                 __ffma2_rn(make_float2(f.z, f.w), make_float2(qs[k], qs[k]),
-                                           make_float2(nm[k], nm[k])));
+                                           __fadd2_rn(ls, make_float2(nm[k], nm[k]))));
                             a = x.x;
                             b = x.y;
                         }
@@ -604,28 +618,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                             tmem_ld16(s_addr + c0 / 2 + c * 16, w);
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                w[e] = pack_bf16(bf16_lo(w[e]) * fr, bf16_hi(w[e]) * fr);
+                            {
+                                const float2 x =
+                                    __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+                                w[e] = pack_f16(x.x * fr, x.y * fr);
+                            }
                             tmem_st16(s_addr + c0 / 2 + c * 16, w);
                         }
                     }
                     uint32_t pk[2][8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float4 f = par[kTile / 2 + cb / 2 + 4 * i];
+                        const float4 f =
+                            reinterpret_cast<const float4 *>(par + 3 * kTile)[cb / 2 + 4 * i + t4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float a = v[k >> 1][4 * i + 2 * (k & 1)];
                             const float b = v[k >> 1][4 * i + 2 * (k & 1) + 1];
-                            float2 sc = make_float2(f.x, f.y), lw = make_float2(f.z, f.w);
+                            float2 is = make_float2(f.x, f.y), vl = make_float2(f.z, f.w);
                             if constexpr (kMasked) {  // a hidden position's NaN must not get through
-                                if (a == -INFINITY) sc.x = lw.x = 0.f;
-                                if (b == -INFINITY) sc.y = lw.y = 0.f;
+                                if (a == -INFINITY) is.x = vl.x = 0.f;
+                                if (b == -INFINITY) is.y = vl.y = 0.f;
                             }
-                            const float2 pe = make_float2(ex2(a), ex2(b));
-                            l2[k] = __fadd2_rn(l2[k], pe);
-                            cr2[k] = __ffma2_rn(pe, lw, cr2[k]);
-                            const float2 w = __fmul2_rn(pe, sc);
-                            pk[k >> 1][2 * i + (k & 1)] = pack_bf16(w.x, w.y);
+                            const float2 w = make_float2(ex2(a), ex2(b));
+                            l2[k] = __ffma2_rn(w, is, l2[k]);
+                            cr2[k] = __ffma2_rn(w, vl, cr2[k]);
+                            pk[k >> 1][2 * i + (k & 1)] = pack_f16(w.x, w.y);
                         }
                     }
                     // P over the columns of S that this warp has read
@@ -658,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             // ---- end of the share: the next one's Q, then this one's output ----
             Kv4Cursor nx = u;
             nx.skip(p, n_seg);
-            if (ok_run && t < n_my) qsum = write_q(nx);
+            if (ok_run && t < n_my) write_q(nx);
             bool done = ok_run;
             if (ok_run) done = wait(SD, seg);
             ++seg;
@@ -710,7 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                 for (int e = 0; e < 32; ++e) o[e] = 0.f;
                 if (read_o) tmem_ld32(lane_base + kColO + c * 32, o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] += cr;
+                for (int e = 0; e < 32; ++e)  // (codes of odd channels were 16 times as large)
+                    o[e] = fmaf(o[e], e & 2 ? 1048576.f : 16777216.f, cr);
                 if constexpr (NCP > 1) {
                     // copies 1.. pass their 32 columns through shared memory (16-byte chunk k of
                     // row r in slot k ^ (r & 7))

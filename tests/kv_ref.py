@@ -157,23 +157,24 @@ def attention(q, k, v, scale=None):
 def attention_bound(q, cache, i, dtype, scale=None):
     """Elementwise bound of the library's error for sequence i.
 
-    bf16: every softmax weight, times V's scale, is rounded to bf16 (half a step, 2^-8) before it
-    multiplies the centred code c - 8; the output is rounded once (2^-8 of itself).  fp32 parts:
-    a score's error is below scale * sum|q_e| * (31 s + |lo|) * 2^-20 (128 products of at most
-    16 + 15 steps and the corrections, each a few 2^-24 of the running sum), which moves every
-    weight by that much relative to itself; 2^-18 covers the sums of weights and the merges."""
+    bf16: the weight of every position, times V's scale, is rounded to fp16 (half a step, 2^-11)
+    before it multiplies the code c; the output is rounded once (2^-8 of itself).  fp32 parts: a
+    score's error is below scale * sum|q_e| * (15 s + |lo|) * 2^-20 (128 products of at most 15
+    steps, each a few 2^-24 of the running sum), which moves every weight by that much relative to
+    itself; 2^-18 covers the sums of weights, their exponentials and logarithms, and the merges.
+    Both act on the codes' part s c and the low values' part of a value separately."""
     k, v = cache.kv[i]
     n, h_q, d = q.shape
     g = h_q // cache.h_kv
     sc = scale if scale else 1 / math.sqrt(d)
     (_, kp), (vc, vp) = cache.parts[i]
     out = attention(q, k, v, scale)
-    mean_abs = attention(q, k, v.abs(), scale)
-    step = kp[..., 0].double().abs() * 31 + kp[..., 1].double().abs()
+    step = kp[..., 0].double().abs() * 15 + kp[..., 1].double().abs()
     worst = step.amax(-1).repeat_interleave(g, 0)[None, :, None]
     err = sc * q.double().abs().sum(-1, keepdim=True) * worst * 2.0 ** -20 + 2.0 ** -18
-    bound = 2 * err * mean_abs + HALF_STEP[dtype] * out.abs()
+    codes = attention(q, k, (vp[..., :1].double() * vc.double()).abs(), scale)
+    parts = codes + attention(q, k, vp[..., 1:].double().abs().expand_as(v), scale)
+    bound = 2 * err * parts + HALF_STEP[dtype] * out.abs()
     if dtype == torch.bfloat16:
-        centred = (vp[..., :1].double() * (vc.double() - 8)).abs()
-        bound = bound + 2.0 ** -8 * attention(q, k, centred, scale)
+        bound = bound + 2.0 ** -11 * codes
     return out, bound

@@ -7,15 +7,15 @@
 // what it takes from HBM), so the codes are spread to fp16 tiles in shared memory once and used by
 // tcgen05.mma (4,096 products per cycle).
 //
-// One persistent CTA per SM, 14 warps; the CTAs share all units' tiles evenly (kv4_common.cuh).
+// One persistent CTA per SM, 10 warps (168 registers a thread); the CTAs share all units' tiles evenly (kv4_common.cuh).
 //   warps 0-3  softmax: TMEM lane r holds MMA row r.  The unit's R rows are placed NCP times
 //              (4 copies up to 32 rows, 2 up to 64, else 1) and each warp handles 128 / NCP
 //              columns of its copy, so a tile's exponentials are spread over all four warps
-//   warps 4-11 expand: each streams 16 positions of every tile (a page) through its own ring of
+//   warps 4-7  expand: each streams 32 positions of every tile (two pages) through its own ring of
 //              cp.async stages and writes them as fp16 into the K and V tiles (128-byte rows of
 //              64 channels, 128-byte swizzle), with the positions' five factors beside them
-//   warp 12    S = Q K^T issuer (Q from TMEM), TMEM owner
-//   warp 13    O += P V issuer (P from TMEM)
+//   warp 8     S = Q K^T issuer (Q from TMEM), TMEM owner
+//   warp 9     O += P V issuer (P from TMEM)
 // A word of 8 codes becomes one 16-byte chunk by 4 ANDs and a shift, its channels in the order
 // 0 4 1 5 2 6 3 7; Q is written to TMEM in the same order and O's columns are read back in it, so
 // no code is ever moved to its own place.
@@ -42,12 +42,12 @@ using namespace tc;
 
 constexpr int kRows = 128;           // MMA M
 constexpr int kTile = 128;           // positions per tile (p.tile)
-constexpr int kExpandWarp = 4;       // first of eight
-constexpr int kExpandWarps = 8;
-constexpr int kSWarp = 12;
-constexpr int kPvWarp = 13;
-constexpr int kThreads = 14 * 32;
-static_assert(kExpandWarps * kPageSize == kTile, "a page per expanding warp");
+constexpr int kExpandWarp = 4;       // first of four
+constexpr int kExpandWarps = 4;
+constexpr int kSWarp = 8;
+constexpr int kPvWarp = 9;
+constexpr int kThreads = 10 * 32;
+constexpr int kPages = kTile / kPageSize / kExpandWarps;  // of a tile, per expanding warp
 constexpr int kStages = 4;           // cp.async ring of an expanding warp
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;      // S / P buffers at 0 and 128
@@ -62,8 +62,9 @@ template <int D>
 struct TcCfg {
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kRow = D / 2;
-    static constexpr int kCodes = kPageSize * kRow;        // one warp's share of K (or V)
-    static constexpr int kStageBytes = 2 * kCodes + 128;   // with its parameters
+    static constexpr int kPageCodes = kPageSize * kRow;
+    static constexpr int kPageBytes = 2 * kPageCodes + 128;  // K, V, parameters of a page
+    static constexpr int kStageBytes = kPages * kPageBytes;  // one warp's share of a tile
     static constexpr int kRing = 4 * kTileBytes;           // after K0 K1 V0 V1
     static constexpr int kPar = kRing + kExpandWarps * kStages * kStageBytes;
     static constexpr int kScratch = kPar + kParSlots * kParFloats * 4;
@@ -103,53 +104,50 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
-// 32 columns of 32 lanes in the accumulator layout of an m16n8 fragment: lane (g, t) of the warp
-// gets rows g + 8 k (k = 0..3), columns 8 i + 2 t and 8 i + 2 t + 1 (i = 0..3) in
+// 8 N columns of 32 lanes in the accumulator layout of an m16n8 fragment (N = 4 or 8): lane (g, t)
+// of the warp gets rows g + 8 k (k = 0..3), columns 8 i + 2 t and 8 i + 2 t + 1 (i < N) in
 // v[k / 2][4 i + 2 (k % 2)] and the element after it.
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[2][16]) {
-    uint32_t r[2][16];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        asm volatile(
-            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-            : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3]), "=r"(r[h][4]),
-              "=r"(r[h][5]), "=r"(r[h][6]), "=r"(r[h][7]), "=r"(r[h][8]), "=r"(r[h][9]),
-              "=r"(r[h][10]), "=r"(r[h][11]), "=r"(r[h][12]), "=r"(r[h][13]), "=r"(r[h][14]),
-              "=r"(r[h][15])
-            : "r"(taddr + ((uint32_t)h << 20))
-            : "memory");
-    // (the values pass through the wait, so no use can move before it)
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0][0]), "+r"(r[0][1]), "+r"(r[0][2]), "+r"(r[0][3]), "+r"(r[0][4]),
-                   "+r"(r[0][5]), "+r"(r[0][6]), "+r"(r[0][7]), "+r"(r[0][8]), "+r"(r[0][9]),
-                   "+r"(r[0][10]), "+r"(r[0][11]), "+r"(r[0][12]), "+r"(r[0][13]), "+r"(r[0][14])
-                 :
-                 : "memory");
-    asm volatile(""
-                 : "+r"(r[0][15]), "+r"(r[1][0]), "+r"(r[1][1]), "+r"(r[1][2]), "+r"(r[1][3]),
-                   "+r"(r[1][4]), "+r"(r[1][5]), "+r"(r[1][6]), "+r"(r[1][7]), "+r"(r[1][8]),
-                   "+r"(r[1][9]), "+r"(r[1][10]), "+r"(r[1][11]), "+r"(r[1][12]), "+r"(r[1][13]),
-                   "+r"(r[1][14]), "+r"(r[1][15])
-                 :
-                 : "memory");
+template <int N>
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[2][4 * N]) {
+    uint32_t r[2][4 * N];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[h][e] = __uint_as_float(r[h][e]);
+        for (int b = 0; b < 4 * N; b += 16)
+            asm volatile(
+                "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                : "=r"(r[h][b]), "=r"(r[h][b + 1]), "=r"(r[h][b + 2]), "=r"(r[h][b + 3]),
+                  "=r"(r[h][b + 4]), "=r"(r[h][b + 5]), "=r"(r[h][b + 6]), "=r"(r[h][b + 7]),
+                  "=r"(r[h][b + 8]), "=r"(r[h][b + 9]), "=r"(r[h][b + 10]), "=r"(r[h][b + 11]),
+                  "=r"(r[h][b + 12]), "=r"(r[h][b + 13]), "=r"(r[h][b + 14]), "=r"(r[h][b + 15])
+                : "r"(taddr + ((uint32_t)h << 20) + 2 * b)
+                : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    // (the values pass through statements after the wait, so no use can move before it)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4 * N; ++e) {
+            asm volatile("" : "+r"(r[h][e])::"memory");
+            v[h][e] = __uint_as_float(r[h][e]);
+        }
 }
 
-// The same layout's pairs of columns, packed to bf16: 16 columns of 32 lanes (lane (g, t): rows
+// The same layout's pairs of columns, packed to fp16: 4 N columns of 32 lanes (lane (g, t): rows
 // g + 8 k, column 4 i + t in w[k / 2][2 i + k % 2]).
-__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&w)[2][8]) {
+template <int N>
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&w)[2][2 * N]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-        asm volatile(
-            "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
-                taddr + ((uint32_t)h << 20)),
-            "r"(w[h][0]), "r"(w[h][1]), "r"(w[h][2]), "r"(w[h][3]), "r"(w[h][4]), "r"(w[h][5]),
-            "r"(w[h][6]), "r"(w[h][7])
-            : "memory");
+#pragma unroll
+        for (int b = 0; b < 2 * N; b += 8)
+            asm volatile(
+                "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                    taddr + ((uint32_t)h << 20) + 2 * b),
+                "r"(w[h][b]), "r"(w[h][b + 1]), "r"(w[h][b + 2]), "r"(w[h][b + 3]),
+                "r"(w[h][b + 4]), "r"(w[h][b + 5]), "r"(w[h][b + 6]), "r"(w[h][b + 7])
+                : "memory");
 }
 
 // Bounded wait, out of the hot code: plain polls (the hardware suspends each for a while and wakes
@@ -181,6 +179,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
     constexpr unsigned FULL = 0xffffffffu;
     constexpr int RPC = kRows / NCP;          // rows per copy
     constexpr int NC = kTile / NCP;           // columns of a softmax warp
+    constexpr int CW = NC < 64 ? NC : 64;     // columns that it holds at a time
+    constexpr int N8 = CW / 8;
     extern __shared__ uint8_t smem_raw[];
     // (an offset from the array, so that accesses stay shared-memory instructions)
     uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
@@ -245,47 +245,53 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
     if (warp >= kExpandWarp && warp < kExpandWarp + kExpandWarps) {
         // ---------------------------------------------------------- copy and expand ----------
         const int ew = warp - kExpandWarp;
-        const uint32_t ring = saddr(smem + C::kRing) + ew * kStages * C::kStageBytes;
-        const uint8_t *ring_p = smem + C::kRing + ew * kStages * C::kStageBytes;
-        Kv4Cursor pc = first;
-        int copied = 0, page;
-        auto look_up = [&]() {  // page of the next tile to copy
-            const int j = pc.t * kTile + ew * kPageSize;
-            page = p.page_size && j < pc.kv_len
-                       ? __ldg(p.block_table + (int64_t)pc.b * p.max_pages + (j >> 4))
-                       : 0;
+        uint8_t *ring = smem + C::kRing + ew * kStages * C::kStageBytes;
+        Kv4Cursor pc = first;  // next tile to copy
+        int64_t unit_row = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h;  // (contiguous)
+        int copied = 0, pages[kPages];
+        auto look_up = [&]() {  // pages of the next tile to copy
+#pragma unroll
+            for (int i = 0; i < kPages; ++i) {
+                const int j = pc.t * kTile + (ew * kPages + i) * kPageSize;
+                pages[i] = p.page_size && j < pc.kv_len
+                               ? __ldg(p.block_table + (int64_t)pc.b * p.max_pages + (j >> 4))
+                               : 0;
+            }
         };
         look_up();
-        int64_t unit_row = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h;  // (contiguous)
         constexpr int Q = C::kRow / 16;  // 16-byte chunks of a row
         // chunk q of row r is kept at q ^ (r / (8 / Q) mod Q): 8 rows' chunks in different banks
         auto raw_at = [](int r, int q) { return r * C::kRow + ((q ^ ((r / (8 / Q)) % Q)) << 4); };
         auto copy_next = [&]() {
             if (copied < n_my) {
-                const uint32_t dst = ring + (copied % kStages) * C::kStageBytes;
-                const int j = pc.t * kTile + ew * kPageSize;
-                int n = pc.kv_len - j;  // positions (rows past the end are zeros)
-                int64_t row0 = unit_row + j;
-                if (p.page_size) {
-                    row0 = ((int64_t)page * p.h_kv + pc.g) * kPageSize;
-                    if (n > 0 && (page < 0 || page >= p.num_pages)) {
-                        if (lane == 0) set_dev_err(p.dev_err, SD_DEVERR_PAGE);
-                        n = 0;
-                    }
-                }
-                if (n <= 0) row0 = 0;
+                const uint32_t dst0 = saddr(ring) + (copied % kStages) * C::kStageBytes;
 #pragma unroll
-                for (int k = 0; k < kPageSize * Q / 32; ++k) {
-                    const int x = lane + 32 * k, r = x / Q, q = x % Q;
+                for (int i = 0; i < kPages; ++i) {
+                    const uint32_t dst = dst0 + i * C::kPageBytes;
+                    const int j = pc.t * kTile + (ew * kPages + i) * kPageSize;
+                    int n = pc.kv_len - j;  // positions (rows past the end are zeros)
+                    int64_t row0 = unit_row + j;
+                    if (p.page_size) {
+                        row0 = ((int64_t)pages[i] * p.h_kv + pc.g) * kPageSize;
+                        if (n > 0 && (pages[i] < 0 || pages[i] >= p.num_pages)) {
+                            if (lane == 0) set_dev_err(p.dev_err, SD_DEVERR_PAGE);
+                            n = 0;
+                        }
+                    }
+                    if (n <= 0) row0 = 0;
+#pragma unroll
+                    for (int k = 0; k < kPageSize * Q / 32; ++k) {
+                        const int x = lane + 32 * k, r = x / Q, q = x % Q;
+                        const bool in = r < n;
+                        const int64_t off = (row0 + (in ? r : 0)) * C::kRow + q * 16;
+                        cp_async16z(dst + raw_at(r, q), p.k + off, in ? 16 : 0);
+                        cp_async16z(dst + C::kPageCodes + raw_at(r, q), p.v + off, in ? 16 : 0);
+                    }
+                    const int r = lane & 15;
                     const bool in = r < n;
-                    const int64_t off = (row0 + (in ? r : 0)) * C::kRow + q * 16;
-                    cp_async16z(dst + raw_at(r, q), p.k + off, in ? 16 : 0);
-                    cp_async16z(dst + C::kCodes + raw_at(r, q), p.v + off, in ? 16 : 0);
+                    cp_async4z(dst + 2 * C::kPageCodes + lane * 4,
+                               (lane < 16 ? p.kp : p.vp) + row0 + (in ? r : 0), in ? 4 : 0);
                 }
-                const int r = lane & 15;
-                const bool in = r < n;
-                cp_async4z(dst + 2 * C::kCodes + lane * 4,
-                       (lane < 16 ? p.kp : p.vp) + row0 + (in ? r : 0), in ? 4 : 0);
                 ++copied;
                 pc.next(p);
                 if (pc.t == 0) unit_row = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h;
@@ -293,46 +299,56 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             }
             cp_async_commit();
         };
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kStages - 1; ++i) copy_next();
-        // lane: row (lane & 15), chunks (lane >> 4), (lane >> 4) + 2
+        // The warp's rows of K (or V) of a stage into a tile.  Lane: row (lane & 15) of each page,
+        // chunks (lane >> 4), (lane >> 4) + 2; word c of chunk q is 16-byte chunk 4 (q & 1) + c of
+        // the row in half q / 2.
         auto expand = [&](const uint8_t *src, uint8_t *dst) {
             const int r = lane & 15;
-            // word c of chunk q is 16-byte chunk 4 (q & 1) + c of the row in half q / 2
-            const uint32_t at = (uint32_t)((ew * kPageSize + r) * 128) |
+            const uint32_t at = (uint32_t)((ew * kPages * kPageSize + r) * 128) |
                                 (uint32_t)((((lane >> 4) * 4) ^ (r & 7)) << 4);
+            uint4 x[kPages][Q / 2];
 #pragma unroll
-            for (int k = 0; k < Q / 2; ++k) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(src + raw_at(r, 2 * k + (lane >> 4)));
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int i = 0; i < kPages; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t w8 = w[c] >> 8;
-                    *reinterpret_cast<uint4 *>(dst + k * kHalfBytes + (at ^ (uint32_t)(c << 4))) =
-                        make_uint4(codes_at<0>(w[c], w8), codes_at<1>(w[c], w8),
-                                   codes_at<2>(w[c], w8), codes_at<3>(w[c], w8));
+                for (int k = 0; k < Q / 2; ++k)
+                    x[i][k] = *reinterpret_cast<const uint4 *>(src + i * C::kPageBytes +
+                                                               raw_at(r, 2 * k + (lane >> 4)));
+#pragma unroll
+            for (int i = 0; i < kPages; ++i)
+#pragma unroll
+                for (int k = 0; k < Q / 2; ++k) {
+                    const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t w8 = w[c] >> 8;
+                        *reinterpret_cast<uint4 *>(dst + i * kPageSize * 128 + k * kHalfBytes +
+                                                   (at ^ (uint32_t)(c << 4))) =
+                            make_uint4(codes_at<0>(w[c], w8), codes_at<1>(w[c], w8),
+                                       codes_at<2>(w[c], w8), codes_at<3>(w[c], w8));
+                    }
                 }
-            }
             fence_async_smem();
             __syncwarp();
         };
+#pragma unroll 1
         for (int t = 0; t < n_my; ++t) {
             const int s = t & 1;
-            copy_next();
-            cp_async_wait<kStages - 1>();
+            cp_async_wait<kStages - 2>();  // (tile t's copies)
             __syncwarp();
-            const uint8_t *st = ring_p + (t % kStages) * C::kStageBytes;
+            const uint8_t *st = ring + (t % kStages) * C::kStageBytes;
             if (t >= 2 && !wait1(KE + s, (t - 2) >> 1)) break;
-            {
-                // Factors of this lane's position.  (Slot t % 4: the softmax of tile t - 4 is
-                // past it, since S of tile t - 2 has completed and that waited for the P V of
-                // tile t - 4.)
-                const uint32_t *par = reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes);
-                // (lanes 0-15 the key's two, lanes 16-31 the value's)
-                const uint32_t w = par[lane];
+            // Factors of the positions.  (Slot t % 4: the softmax of tile t - 4 is past it, since
+            // S of tile t - 2 has completed and that waited for the P V of tile t - 4.)
+#pragma unroll
+            for (int i = 0; i < kPages; ++i) {
+                // lanes 0-15 the key's two, lanes 16-31 the value's three
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                    st + i * C::kPageBytes + 2 * C::kPageCodes + lane * 4);
                 const float lw = param_low(w);
                 float sc = param_scale(w);
-                const int j = ew * kPageSize + (lane & 15);
+                const int j = (ew * kPages + i) * kPageSize + (lane & 15);
                 float *d = s_par + (t % kParSlots) * kParFloats + (j >> 1) * 4 + (j & 1);
                 if (lane < 16) {
                     d[0] = sc * p.scale_log2;
@@ -347,8 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             }
             expand(st, sK + s * C::kTileBytes);
             if (lane == 0) mbar_arrive(BAR(KF + s));
+            copy_next();  // (while S is computed; into the stage that tile t - 1 has left)
             if (t >= 2 && !wait1(PD + s, (t - 2) >> 1)) break;
-            expand(st + C::kCodes, sV + s * C::kTileBytes);
+            expand(st + C::kPageCodes, sV + s * C::kTileBytes);
             if (lane == 0) mbar_arrive(BAR(VF + s));
         }
         cp_async_wait<0>();
@@ -367,13 +384,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             if (!ok) break;
             tc_after();
             if (lane == 0) {
-                uint32_t kb = saddr(sK + s * C::kTileBytes);
-#pragma unroll 1
-                for (int h = 0; h < D / 64; ++h, kb += kHalfBytes)
-#pragma unroll 1
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(tmem + s * kTile, tmem + kColQ + (h * 4 + kk) * 8,
-                               desc_k_sw128(kb + kk * 32), idesc, h + kk > 0 ? 1u : 0u);
+                const uint32_t kb = saddr(sK + s * C::kTileBytes);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ts(tmem + s * kTile, tmem + kColQ + kk * 8,
+                           desc_k_sw128(kb + (kk >> 2) * kHalfBytes + (kk & 3) * 32), idesc,
+                           kk > 0 ? 1u : 0u);
                 mma_commit(BAR(SF + s));
                 mma_commit(BAR(KE + s));
                 mbar_arrive(BAR(SF + s));  // (orders the factors before the softmax's reads)
@@ -403,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             const bool last = t + 1 == n_my || c.t + 1 == c.tiles;
             if (lane == 0) {
                 const uint32_t vb = saddr(sV + s * C::kTileBytes);
-#pragma unroll 1
+#pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
                     mma_ts(tmem + kColO, tmem + s * kTile + kk * 8,
                            desc_mn_sw128(vb + kk * 2048, kHalfBytes), idesc,
@@ -526,15 +542,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                 const int p0 = lt * kTile;
                 // every row sees every position of the tile (rows past R may compute anything)
                 const bool interior = p0 + kTile - 1 <= first_limit;
-                // 32 columns (instantiated apart for tiles that need no mask); false: a wait failed
+                // CW columns (instantiated apart for tiles that need no mask); false: a wait failed
                 auto chunk = [&](int ch, auto masked) {
                     constexpr bool kMasked = decltype(masked)::value;
-                    const int cb = c0 + ch * 32;
-                    float v[2][16];
-                    tmem_ld_frag(s_addr + cb, v);
+                    const int cb = c0 + ch * CW;
+                    float v[2][4 * N8];
+                    tmem_ld_frag<N8>(s_addr + cb, v);
                     // exponents of the weights: x + log2 s - m
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < N8; ++i) {
                         const int at = cb / 2 + 4 * i + t4;  // the pair of positions
                         const float4 f = reinterpret_cast<const float4 *>(par)[at];
                         const float2 ls = reinterpret_cast<const float2 *>(par + 2 * kTile)[at];
@@ -553,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                     }
                     if constexpr (kMasked) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < N8; ++i)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -565,9 +581,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                     bool grow = false;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float *x = &v[k >> 1][2 * (k & 1)];
-                        mx[k] = max3(max3(x[0], x[1], x[4]), max3(x[5], x[8], x[9]),
-                                     fmaxf(x[12], x[13]));
+                        mx[k] = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < N8; ++i)
+                            mx[k] = max3(mx[k], v[k >> 1][4 * i + 2 * (k & 1)],
+                                         v[k >> 1][4 * i + 2 * (k & 1) + 1]);
                         // (before a row's first visible position its maximum is -inf and nm is 0)
                         grow |= mx[k] > (mk[k] == -INFINITY ? -INFINITY : kRescaleLog2);
                     }
@@ -583,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                                 mk[k] = x - nm[k];
                                 nm[k] = -mk[k];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
+                                for (int i = 0; i < N8; ++i)
 #pragma unroll
                                     for (int c = 0; c < 2; ++c) v[k >> 1][4 * i + 2 * (k & 1) + c] -= x;
                             }
@@ -613,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                         }
                         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 #pragma unroll 1
-                        for (int c = 0; c < ch; ++c) {  // this tile's weights so far
+                        for (int c = 0; c < ch * (CW / 32); ++c) {  // this tile's weights so far
                             uint32_t w[16];
                             tmem_ld16(s_addr + c0 / 2 + c * 16, w);
 #pragma unroll
@@ -626,9 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                             tmem_st16(s_addr + c0 / 2 + c * 16, w);
                         }
                     }
-                    uint32_t pk[2][8];
+                    uint32_t pk[2][2 * N8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < N8; ++i) {
                         const float4 f =
                             reinterpret_cast<const float4 *>(par + 3 * kTile)[cb / 2 + 4 * i + t4];
 #pragma unroll
@@ -647,16 +665,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                         }
                     }
                     // P over the columns of S that this warp has read
-                    tmem_st_frag(s_addr + cb / 2, pk);
+                    tmem_st_frag<N8>(s_addr + cb / 2, pk);
                     return true;
                 };
                 if (interior) {
 #pragma unroll 1
-                    for (int ch = 0; ok_run && ch < NC / 32; ++ch)
+                    for (int ch = 0; ok_run && ch < NC / CW; ++ch)
                         ok_run = chunk(ch, std::false_type{});
                 } else {
 #pragma unroll 1
-                    for (int ch = 0; ok_run && ch < NC / 32; ++ch)
+                    for (int ch = 0; ok_run && ch < NC / CW; ++ch)
                         ok_run = chunk(ch, std::true_type{});
                 }
                 if (!ok_run) break;

@@ -7,15 +7,17 @@
 // what it takes from HBM), so the codes are spread to fp16 tiles in shared memory once and used by
 // tcgen05.mma (4,096 products per cycle).
 //
-// One persistent CTA per SM, 10 warps (168 registers a thread); the CTAs share all units' tiles evenly (kv4_common.cuh).
+// One persistent CTA per SM, 11 warps (168 registers a thread); the CTAs share all units'
+// tiles evenly (kv4_common.cuh).
 //   warps 0-3  softmax: TMEM lane r holds MMA row r.  The unit's R rows are placed NCP times
 //              (4 copies up to 32 rows, 2 up to 64, else 1) and each warp handles 128 / NCP
 //              columns of its copy, so a tile's exponentials are spread over all four warps
-//   warps 4-7  expand: each streams 32 positions of every tile (two pages) through its own ring of
-//              cp.async stages and writes them as fp16 into the K and V tiles (128-byte rows of
-//              64 channels, 128-byte swizzle), with the positions' five factors beside them
+//   warps 4-7  expand: each takes 32 positions of every tile from the ring and writes them as fp16
+//              into the K and V tiles (128-byte rows of 64 channels, 128-byte swizzle), with the
+//              positions' five factors beside them
 //   warp 8     S = Q K^T issuer (Q from TMEM), TMEM owner
 //   warp 9     O += P V issuer (P from TMEM)
+//   warp 10    copies tiles up to kStages ahead: one bulk copy per page for the codes of K and of V
 // A word of 8 codes becomes one 16-byte chunk by 4 ANDs and a shift, its channels in the order
 // 0 4 1 5 2 6 3 7; Q is written to TMEM in the same order and O's columns are read back in it, so
 // no code is ever moved to its own place.
@@ -46,9 +48,12 @@ constexpr int kExpandWarp = 4;       // first of four
 constexpr int kExpandWarps = 4;
 constexpr int kSWarp = 8;
 constexpr int kPvWarp = 9;
-constexpr int kThreads = 10 * 32;
-constexpr int kPages = kTile / kPageSize / kExpandWarps;  // of a tile, per expanding warp
-constexpr int kStages = 4;           // cp.async ring of an expanding warp
+constexpr int kCopyWarp = 10;
+constexpr int kThreads = 11 * 32;
+constexpr int kWarpRows = kTile / kExpandWarps;  // positions of a tile, per expanding warp
+static_assert(kWarpRows == 32, "a lane makes one position's factors");
+constexpr int kPages = kTile / kPageSize;
+constexpr int kStages = 4;           // ring of tiles in flight
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;      // S / P buffers at 0 and 128
 constexpr uint32_t kColQ = 384;
@@ -62,11 +67,10 @@ template <int D>
 struct TcCfg {
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kRow = D / 2;
-    static constexpr int kPageCodes = kPageSize * kRow;
-    static constexpr int kPageBytes = 2 * kPageCodes + 128;  // K, V, parameters of a page
-    static constexpr int kStageBytes = kPages * kPageBytes;  // one warp's share of a tile
+    static constexpr int kCodes = kTile * kRow;                 // K's codes of a tile
+    static constexpr int kStageBytes = 2 * kCodes + 8 * kTile;  // K, V, parameters of K and V
     static constexpr int kRing = 4 * kTileBytes;           // after K0 K1 V0 V1
-    static constexpr int kPar = kRing + kExpandWarps * kStages * kStageBytes;
+    static constexpr int kPar = kRing + kStages * kStageBytes;
     static constexpr int kScratch = kPar + kParSlots * kParFloats * 4;
     // maxima and sums of every MMA row, then 32 columns of the copies' outputs
     static constexpr int kScratchBytes = (2 * kRows + 96 * 32) * 4;
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
     constexpr unsigned FULL = 0xffffffffu;
     constexpr int RPC = kRows / NCP;          // rows per copy
     constexpr int NC = kTile / NCP;           // columns of a softmax warp
-    constexpr int CW = NC < 64 ? NC : 64;     // columns that it holds at a time
+    constexpr int CW = NC < 32 ? NC : 32;     // columns that it holds at a time
     constexpr int N8 = CW / 8;
     extern __shared__ uint8_t smem_raw[];
     // (an offset from the array, so that accesses stay shared-memory instructions)
@@ -196,6 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
     // K written, K read (S computed), V written, S computed, P written, P V computed (V read and
     // the S / P buffer free), per buffer; then a unit's share done, Q written, two drains
     constexpr int KF = 0, KE = 2, VF = 4, SF = 6, PF = 8, PD = 10, SD = 12, QF = 13, DR = 14, DS = 15;
+    // a stage of the ring filled, and read
+    constexpr int RF = 16, RE = RF + kStages;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.group;
     const int n_active = NCP > 1 ? 4 : min(4, (G * p.max_q_rows + 31) / 32);
@@ -220,6 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             mbar_init(BAR(PF + s), 32 * n_active);
             mbar_init(BAR(PD + s), 1);
         }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(BAR(RF + i), 64);  // (two arrivals of each lane of the copying warp)
+            mbar_init(BAR(RE + i), kExpandWarps);
+        }
         mbar_init(BAR(SD), 1);
         mbar_init(BAR(QF), 32 * n_active);
         mbar_init(BAR(DR), 1);
@@ -243,132 +253,145 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
     };
 
     if (warp >= kExpandWarp && warp < kExpandWarp + kExpandWarps) {
-        // ---------------------------------------------------------- copy and expand ----------
+        // ---------------------------------------------------------- expand --------------------
         const int ew = warp - kExpandWarp;
-        uint8_t *ring = smem + C::kRing + ew * kStages * C::kStageBytes;
-        Kv4Cursor pc = first;  // next tile to copy
-        int64_t unit_row = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h;  // (contiguous)
-        int copied = 0, pages[kPages];
-        auto look_up = [&]() {  // pages of the next tile to copy
-#pragma unroll
-            for (int i = 0; i < kPages; ++i) {
-                const int j = pc.t * kTile + (ew * kPages + i) * kPageSize;
-                pages[i] = p.page_size && j < pc.kv_len
-                               ? __ldg(p.block_table + (int64_t)pc.b * p.max_pages + (j >> 4))
-                               : 0;
-            }
-        };
-        look_up();
-        constexpr int Q = C::kRow / 16;  // 16-byte chunks of a row
-        // chunk q of row r is kept at q ^ (r / (8 / Q) mod Q): 8 rows' chunks in different banks
-        auto raw_at = [](int r, int q) { return r * C::kRow + ((q ^ ((r / (8 / Q)) % Q)) << 4); };
-        auto copy_next = [&]() {
-            if (copied < n_my) {
-                const uint32_t dst0 = saddr(ring) + (copied % kStages) * C::kStageBytes;
-#pragma unroll
-                for (int i = 0; i < kPages; ++i) {
-                    const uint32_t dst = dst0 + i * C::kPageBytes;
-                    const int j = pc.t * kTile + (ew * kPages + i) * kPageSize;
-                    int n = pc.kv_len - j;  // positions (rows past the end are zeros)
-                    int64_t row0 = unit_row + j;
-                    if (p.page_size) {
-                        row0 = ((int64_t)pages[i] * p.h_kv + pc.g) * kPageSize;
-                        if (n > 0 && (pages[i] < 0 || pages[i] >= p.num_pages)) {
-                            if (lane == 0) set_dev_err(p.dev_err, SD_DEVERR_PAGE);
-                            n = 0;
-                        }
-                    }
-                    if (n <= 0) row0 = 0;
-#pragma unroll
-                    for (int k = 0; k < kPageSize * Q / 32; ++k) {
-                        const int x = lane + 32 * k, r = x / Q, q = x % Q;
-                        const bool in = r < n;
-                        const int64_t off = (row0 + (in ? r : 0)) * C::kRow + q * 16;
-                        cp_async16z(dst + raw_at(r, q), p.k + off, in ? 16 : 0);
-                        cp_async16z(dst + C::kPageCodes + raw_at(r, q), p.v + off, in ? 16 : 0);
-                    }
-                    const int r = lane & 15;
-                    const bool in = r < n;
-                    cp_async4z(dst + 2 * C::kPageCodes + lane * 4,
-                               (lane < 16 ? p.kp : p.vp) + row0 + (in ? r : 0), in ? 4 : 0);
-                }
-                ++copied;
-                pc.next(p);
-                if (pc.t == 0) unit_row = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h;
-                if (copied < n_my) look_up();
-            }
-            cp_async_commit();
-        };
-#pragma unroll 1
-        for (int i = 0; i < kStages - 1; ++i) copy_next();
-        // The warp's rows of K (or V) of a stage into a tile.  Lane: row (lane & 15) of each page,
-        // chunks (lane >> 4), (lane >> 4) + 2; word c of chunk q is 16-byte chunk 4 (q & 1) + c of
-        // the row in half q / 2.
+        constexpr int Q = C::kRow / 16;       // 16-byte chunks of a row
+        constexpr int kLoads = kWarpRows * Q / 32;
+        // The warp's rows of K (or V) of a stage into a tile.  Load i of the warp is 32 / Q rows in
+        // a piece: lane has chunk lane % Q of row lane / Q.  Word c of chunk q is 16-byte chunk
+        // 4 (q & 1) + c of the row in half q / 2; lanes of the second half take their words in
+        // the order 2 3 0 1, so that 8 lanes' stores fall into different banks.
+        const int er = lane / Q, eq = lane % Q;
+        const bool swap = eq >= 2;
+        const uint32_t at = (uint32_t)((ew * kWarpRows + er) * 128) + (uint32_t)(eq >> 1) * kHalfBytes +
+                            (uint32_t)((((eq & 1) * 4) ^ (swap ? 2 : 0) ^ (er & 7)) << 4);
         auto expand = [&](const uint8_t *src, uint8_t *dst) {
-            const int r = lane & 15;
-            const uint32_t at = (uint32_t)((ew * kPages * kPageSize + r) * 128) |
-                                (uint32_t)((((lane >> 4) * 4) ^ (r & 7)) << 4);
-            uint4 x[kPages][Q / 2];
+            uint4 x[kLoads];
 #pragma unroll
-            for (int i = 0; i < kPages; ++i)
+            for (int i = 0; i < kLoads; ++i)
+                x[i] = *reinterpret_cast<const uint4 *>(src + ew * kWarpRows * C::kRow + i * 512 +
+                                                        lane * 16);
 #pragma unroll
-                for (int k = 0; k < Q / 2; ++k)
-                    x[i][k] = *reinterpret_cast<const uint4 *>(src + i * C::kPageBytes +
-                                                               raw_at(r, 2 * k + (lane >> 4)));
+            for (int i = 0; i < kLoads; ++i) {
+                const uint32_t w[4] = {swap ? x[i].z : x[i].x, swap ? x[i].w : x[i].y,
+                                       swap ? x[i].x : x[i].z, swap ? x[i].y : x[i].w};
 #pragma unroll
-            for (int i = 0; i < kPages; ++i)
-#pragma unroll
-                for (int k = 0; k < Q / 2; ++k) {
-                    const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t w8 = w[c] >> 8;
-                        *reinterpret_cast<uint4 *>(dst + i * kPageSize * 128 + k * kHalfBytes +
-                                                   (at ^ (uint32_t)(c << 4))) =
-                            make_uint4(codes_at<0>(w[c], w8), codes_at<1>(w[c], w8),
-                                       codes_at<2>(w[c], w8), codes_at<3>(w[c], w8));
-                    }
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t w8 = w[c] >> 8;
+                    // (32 / Q rows on; the swizzle of row r is r mod 8, and 32 / Q is 8 or 16)
+                    *reinterpret_cast<uint4 *>(dst + i * (32 / Q) * 128 +
+                                               (at ^ (uint32_t)(c << 4))) =
+                        make_uint4(codes_at<0>(w[c], w8), codes_at<1>(w[c], w8),
+                                   codes_at<2>(w[c], w8), codes_at<3>(w[c], w8));
                 }
+            }
             fence_async_smem();
             __syncwarp();
         };
 #pragma unroll 1
         for (int t = 0; t < n_my; ++t) {
             const int s = t & 1;
-            cp_async_wait<kStages - 2>();  // (tile t's copies)
-            __syncwarp();
-            const uint8_t *st = ring + (t % kStages) * C::kStageBytes;
-            if (t >= 2 && !wait1(KE + s, (t - 2) >> 1)) break;
-            // Factors of the positions.  (Slot t % 4: the softmax of tile t - 4 is past it, since
-            // S of tile t - 2 has completed and that waited for the P V of tile t - 4.)
-#pragma unroll
-            for (int i = 0; i < kPages; ++i) {
-                // lanes 0-15 the key's two, lanes 16-31 the value's three
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(
-                    st + i * C::kPageBytes + 2 * C::kPageCodes + lane * 4);
-                const float lw = param_low(w);
-                float sc = param_scale(w);
-                const int j = (ew * kPages + i) * kPageSize + (lane & 15);
-                float *d = s_par + (t % kParSlots) * kParFloats + (j >> 1) * 4 + (j & 1);
-                if (lane < 16) {
-                    d[0] = sc * p.scale_log2;
-                    d[2] = lw * p.scale_log2;
-                } else {
+            const uint8_t *st = smem + C::kRing + (t % kStages) * C::kStageBytes;
+            if (!wait1(RF + t % kStages, t / kStages)) break;
+            bool ok = true;
+#pragma unroll 1
+            for (int v = 0; v < 2; ++v) {  // K, then V (one copy of the code)
+                ok = t < 2 || wait1((v ? PD : KE) + s, (t - 2) >> 1);
+                if (!ok) break;
+                if (v == 0) {
+                    // Factors of the positions.  (Slot t % 4: the softmax of tile t - 4 is past it,
+                    // since S of tile t - 2 has completed and that waited for the P V of tile
+                    // t - 4.)
+                    const int j = ew * kWarpRows + lane;
+                    const uint32_t *w = reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes) + j;
+                    const uint32_t wk = w[0], wv = w[kTile];
+                    float *f = s_par + (t % kParSlots) * kParFloats;
+                    float *d = f + (j >> 1) * 4 + (j & 1);
+                    d[0] = param_scale(wk) * p.scale_log2;
+                    d[2] = param_low(wk) * p.scale_log2;
+                    float sc = param_scale(wv);
                     sc = sc == 0.f ? 1.f : fmaxf(sc, kMinScale);
                     const float inv = rcp(sc);
-                    s_par[(t % kParSlots) * kParFloats + 2 * kTile + j] = lg2(sc);
+                    f[2 * kTile + j] = lg2(sc);
                     d[3 * kTile] = inv;
-                    d[3 * kTile + 2] = lw * inv;
+                    d[3 * kTile + 2] = param_low(wv) * inv;
                 }
+                expand(st + v * C::kCodes, (v ? sV : sK) + s * C::kTileBytes);
+                if (lane == 0) mbar_arrive(BAR((v ? VF : KF) + s));
             }
-            expand(st, sK + s * C::kTileBytes);
-            if (lane == 0) mbar_arrive(BAR(KF + s));
-            copy_next();  // (while S is computed; into the stage that tile t - 1 has left)
-            if (t >= 2 && !wait1(PD + s, (t - 2) >> 1)) break;
-            expand(st + C::kPageCodes, sV + s * C::kTileBytes);
-            if (lane == 0) mbar_arrive(BAR(VF + s));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(BAR(RE + t % kStages));
         }
-        cp_async_wait<0>();
+    } else if (warp == kCopyWarp) {
+        // ---------------------------------------------------------- copy ----------------------
+        // Lane: page (lane & 7) of the tile, of K (lanes 0-7) or V (lanes 8-15); then positions
+        // lane + 32 k of both for the parameters.  Codes of rows past the end stay as they were
+        // (any nibble is a finite number, and the softmax gives it the weight zero); parameters
+        // are zeros there.
+        Kv4Cursor pc = first;
+        int64_t unit_row = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h;  // (contiguous)
+        auto look_up = [&]() {  // this lane's page of the next tile
+            const int j = pc.t * kTile + (lane & 7) * kPageSize;
+            return p.page_size && j < pc.kv_len
+                       ? __ldg(p.block_table + (int64_t)pc.b * p.max_pages + (j >> 4))
+                       : 0;
+        };
+        int page = look_up();
+        int issued = 0;
+#pragma unroll 1
+        for (; issued < n_my; ++issued) {
+            const int st = issued % kStages;
+            if (issued >= kStages && !wait1(RE + st, issued / kStages - 1)) break;
+            uint8_t *stage = smem + C::kRing + st * C::kStageBytes;
+            const uint32_t dst = saddr(stage);
+            const int j = (lane & 7) * kPageSize;
+            const int left = pc.kv_len - pc.t * kTile;  // positions of the tile, 128 or more: all
+            int n = min(max(left - j, 0), kPageSize);
+            int64_t row0 = unit_row + pc.t * kTile + j;
+            bool bad = false;
+            if (p.page_size) {
+                bad = n > 0 && (page < 0 || page >= p.num_pages);
+                row0 = ((int64_t)page * p.h_kv + pc.g) * kPageSize;
+            }
+            const uint32_t my = dst + (lane >> 3) * C::kCodes + j * C::kRow;
+            if (lane < 16 && bad) {  // a page outside the pool reads as zeros
+                set_dev_err(p.dev_err, SD_DEVERR_PAGE);
+                uint8_t *z = stage + (lane >> 3) * C::kCodes + j * C::kRow;
+                for (int i = 0; i < kPageSize * C::kRow; i += 16)
+                    *reinterpret_cast<uint4 *>(z + i) = make_uint4(0u, 0u, 0u, 0u);
+                fence_async_smem();
+            }
+            if (bad) n = 0;
+            const uint32_t bytes = lane < 16 ? (uint32_t)(n * C::kRow) : 0u;
+            mbar_arrive_tx(BAR(RF + st), bytes);
+            if (bytes)
+                bulk_load(my, (lane < 8 ? p.k : p.v) + row0 * C::kRow, bytes, BAR(RF + st));
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k) {
+                const int from = 2 * k + (lane >> 4);  // the page's lane
+                const int64_t row = __shfl_sync(FULL, row0, from) + (lane & 15);
+                const bool in = (lane & 15) < __shfl_sync(FULL, n, from);
+                const uint32_t d = dst + 2 * C::kCodes + (lane + 32 * k) * 4;
+                cp_async4z(d, p.kp + (in ? row : 0), in ? 4 : 0);
+                cp_async4z(d + 4 * kTile, p.vp + (in ? row : 0), in ? 4 : 0);
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(BAR(RF + st))
+                         : "memory");
+            pc.next(p);
+            if (pc.t == 0) unit_row = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h;
+            if (issued + 1 < n_my) page = look_up();
+        }
+        // the copies in flight
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            const unsigned long long t0 = now_ns();
+            for (int i = max(issued - kStages, 0); i < issued; ++i)
+                while (!mbar_try(BAR(RF + i % kStages), (i / kStages) & 1) &&
+                       now_ns() - t0 < kDrainNs) {
+                }
+        }
+        __syncwarp();
     } else if (warp == kSWarp) {
         // ---------------------------------------------------------- S = Q K^T issuer ---------
         const uint32_t idesc = idesc_f16(kTile, false);
@@ -546,14 +569,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                 auto chunk = [&](int ch, auto masked) {
                     constexpr bool kMasked = decltype(masked)::value;
                     const int cb = c0 + ch * CW;
+                    // (all of the positions' factors at once, ahead of their use: one warp per
+                    // issue slot has nothing else to cover their latency)
+                    float4 kf[N8];
+                    float2 ls[N8];
+#pragma unroll
+                    for (int i = 0; i < N8; ++i) {
+                        const int at = cb / 2 + 4 * i + t4;  // the pair of positions
+                        kf[i] = reinterpret_cast<const float4 *>(par)[at];
+                        ls[i] = reinterpret_cast<const float2 *>(par + 2 * kTile)[at];
+                    }
+                    float4 vf[N8];
+#pragma unroll
+                    for (int i = 0; i < N8; ++i)
+                        vf[i] = reinterpret_cast<const float4 *>(par + 3 * kTile)[cb / 2 + 4 * i + t4];
                     float v[2][4 * N8];
                     tmem_ld_frag<N8>(s_addr + cb, v);
                     // exponents of the weights: x + log2 s - m
 #pragma unroll
                     for (int i = 0; i < N8; ++i) {
-                        const int at = cb / 2 + 4 * i + t4;  // the pair of positions
-                        const float4 f = reinterpret_cast<const float4 *>(par)[at];
-                        const float2 ls = reinterpret_cast<const float2 *>(par + 2 * kTile)[at];
+                        const float4 f = kf[i];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             float &a = v[k >> 1][4 * i + 2 * (k & 1)];
@@ -562,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                                 __fmul2_rn(make_float2(a, b), make_float2(qe[k], qe[k])),
                                 make_float2(f.x, f.y),
                                 __ffma2_rn(make_float2(f.z, f.w), make_float2(qs[k], qs[k]),
-                                           __fadd2_rn(ls, make_float2(nm[k], nm[k]))));
+                                           __fadd2_rn(ls[i], make_float2(nm[k], nm[k]))));
                             a = x.x;
                             b = x.y;
                         }
@@ -647,8 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                     uint32_t pk[2][2 * N8];
 #pragma unroll
                     for (int i = 0; i < N8; ++i) {
-                        const float4 f =
-                            reinterpret_cast<const float4 *>(par + 3 * kTile)[cb / 2 + 4 * i + t4];
+                        const float4 f = vf[i];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float a = v[k >> 1][4 * i + 2 * (k & 1)];

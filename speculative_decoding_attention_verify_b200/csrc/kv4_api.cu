@@ -159,13 +159,19 @@ sd_status plan_kv4(const sd_q_desc *q, const sd_kv4_desc *kv, int batch, Kv4Plan
         if (plan->tcgen05)
             kv4_tc_plan(&plan->tile, &per_sm);
         else
-            kv4_mma_plan(kv->head_dim, (int)rows, &plan->tile, &per_sm);
+            kv4_mma_plan(&plan->tile, &per_sm);
         const long long per_unit = ((long long)q->max_kv_len + plan->tile - 1) / plan->tile;
         const long long units = (long long)batch * kv->h_kv;
         const long long slots = (long long)device_sm_count() * per_sm;
-        // Up to four tiles per unit: whole units per CTA.  (A unit's further tiles cost about
-        // 1 us each; the merge is a launch of its own, 3 us, after partial results.)
-        plan->whole = per_unit <= 4;
+        // Whole units per CTA, where the longest CTA then has few tiles more than with an even
+        // share of all tiles: a share's end, its partial results and the launch that merges them
+        // cost about as much as 4 tiles of the mma.sync kernel or 8 of the tcgen05 one.  (28
+        // sequences, 4 KV heads: 7 rows at 1,024 positions 12.5 us whole, 18.2 shared, at 2,048
+        // 17.3 and 20.7; 63 rows at 1,024 23.1 and 45.7.  8 sequences of 4,096, 7 rows: 26.7 and
+        // 17.6.)  Not beyond 16 tiles, since sequences shorter than the hint leave CTAs idle.
+        const long long longest = (units + slots - 1) / slots * per_unit;
+        const long long even = (units * per_unit + slots - 1) / slots;
+        plan->whole = per_unit <= 16 && longest <= even + (plan->tcgen05 ? 8 : 4);
         const long long n = plan->whole ? units : units * per_unit;
         plan->ctas = (int)(n < slots ? n : slots);
     }

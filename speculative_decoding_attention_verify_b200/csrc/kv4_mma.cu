@@ -27,17 +27,14 @@
 // one 8x8 transpose per 8 positions.  (mma.sync runs at 1,024 products per cycle per SM here, a
 // quarter of tcgen05's rate; at 8 rows that is a third of the time that a tile takes from HBM.)
 //
-// Work.  The CTAs share all units' tiles evenly (kv4_common.cuh).  A CTA's 8 warps are row blocks
-// (up to 8 NT rows each, NT = 1, 2 or 4) x slots of positions: of every tile a warp takes the 32
-// positions (two pages) of its slot for the rows of its block.  Warps of one slot expand the same
-// codes each for itself: with 32 rows to use them the expansion is a third of the work, and no
-// warp ever waits for another.  Each warp streams its positions through its own two cp.async
-// stages, with its page numbers looked up a stage further ahead, and keeps its own running maxima,
-// sums and O^T; there is no block-wide step until a unit ends, where the slots are merged pairwise
-// through shared memory.  The maximum moves only when a score exceeds it by more than 2^16 (one
-// vote per 32 positions; a weight stays finite in bf16 far beyond that).
-// Query fragments are registers for NT = 1; for more they are read from shared memory, once for
-// both pages.
+// Work.  The CTAs share all units' tiles evenly (kv4_common.cuh); of every tile each of a CTA's 8
+// warps takes 32 positions (two pages) for all rows.  Each warp streams its positions through its
+// own two cp.async stages, with its page numbers looked up a stage further ahead, and keeps its own
+// running maxima, sums and O^T; there is no block-wide step until a unit ends, where the warps'
+// shares are merged pairwise through shared memory.  The maximum moves only when a score exceeds
+// it by more than 2^14 (one vote per 32 positions; a weight stays finite in fp16).
+// Query fragments are registers for up to 8 rows; for more they are read from shared memory, once
+// for both pages.
 #include <type_traits>
 
 #include "kv4_common.cuh"
@@ -56,8 +53,8 @@ constexpr int kPos = 32;       // positions of a warp per tile
 constexpr int kStages = 2;
 constexpr float kGrow = 14.0f;  // weights stay below fp16's largest number
 
-// CTAs per SM: registers of O^T decide.
-constexpr int ctas_per_sm(int nt) { return nt < 4 ? 2 : 1; }
+constexpr int kTile = kWarps * kPos;
+constexpr int kCtasPerSm = 2;  // registers of O^T decide
 
 template <int D, int NT>
 struct MmaCfg {
@@ -69,12 +66,11 @@ struct MmaCfg {
     static constexpr int kMt = D / 16;                     // channel tiles of O^T, k steps of S^T
     static constexpr int kOFloats = kMt * NT * 4;          // O^T values of a lane
     static constexpr int kPart = (kOFloats + 6 * NT) * 32;  // floats of one warp's partial
-    // query fragments: registers for NT = 1, of one row block for 2, of up to four for 4
+    // query fragments: registers for NT = 1
     static constexpr int kQ = kRing + kWarps / 2 * kPart * 4;
-    static constexpr int kSmem = kQ + (NT == 1 ? 0 : NT == 2 ? 1 : 4) * NT * kMt * 256;
+    static constexpr int kSmem = kQ + (NT == 1 ? 0 : NT * kMt * 256);
 };
-static_assert(2 * (MmaCfg<128, 2>::kSmem + 1024) <= 227 * 1024, "two CTAs per SM");
-static_assert(MmaCfg<128, 4>::kSmem <= 226 * 1024, "shared memory");
+static_assert(kCtasPerSm * (MmaCfg<128, 2>::kSmem + 1024) <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -97,7 +93,7 @@ __device__ __forceinline__ int m_of(int r) { return (r & 8) | ((r & 3) << 1) | (
 __device__ __forceinline__ int pos_of(int m) { return (m & 8) | ((m & 1) << 2) | ((m >> 1) & 3); }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
 kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
     pdl_trigger();  // (see launch_pdl)
     pdl_wait();
@@ -111,8 +107,6 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
     __shared__ Kv4Start s_start;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gq = lane >> 2, t4 = lane & 3;
-    const int slots = p.tile / kPos, blocks = kWarps / slots;  // position slots, row blocks
-    const int rb = warp % blocks, slot = warp / blocks;
 
     long long lo, hi;
     Kv4Cursor cc = kv4_first<kThreads>(p, s_red, &s_start, lo, hi);  // next tile to compute
@@ -138,7 +132,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
     auto look_up = [&]() {  // pages of the next tile to copy
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int j = pc.t * p.tile + slot * kPos + i * kPageSize;
+            const int j = pc.t * kTile + warp * kPos + i * kPageSize;
             pages[i] = p.page_size && j < pc.kv_len
                            ? __ldg(p.block_table + (int64_t)pc.b * p.max_pages + (j >> 4))
                            : 0;
@@ -149,7 +143,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
     int64_t unit_row = (int64_t)pc.b * p.stride_b + (int64_t)pc.g * p.stride_h;  // (contiguous)
     auto copy_next = [&]() {
         if (copied < n_my) {
-            const int j0 = pc.t * p.tile + slot * kPos;
+            const int j0 = pc.t * kTile + warp * kPos;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int j = j0 + i * kPageSize;
@@ -199,7 +193,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
 #pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) copy_next();
 
-    uint2 *s_q = reinterpret_cast<uint2 *>(smem + C::kQ) + rb * NT * kKs * 32;
+    uint2 *s_q = reinterpret_cast<uint2 *>(smem + C::kQ);
     int done = 0;
 #pragma unroll 1
     while (done < n_my) {
@@ -207,14 +201,13 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
         const int n_seg = min(cc.tiles - cc.t, n_my - done);
         const bool starts = cc.t == 0, ends = cc.t + n_seg == cc.tiles;
         const int G = p.group, R = cc.n_q * G, kv_len = cc.kv_len;
-        const int r_base = rb * 8 * NT;  // first row of the block
         // the last position that query row 0 sees: positions up to it need no mask
         const int first_limit = kv_len - cc.n_q;
         uint32_t qb[kQRegs ? kKs : 1][2];
         float2 qs[NT], qe[NT];  // of columns 2t, 2t + 1: sums of the query, 2^24 / its scale
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = r_base + nt * 8 + gq;
+            const int r = nt * 8 + gq;
             const bool has = r < R;
             const uint4 *src = reinterpret_cast<const uint4 *>(
                 static_cast<const unsigned short *>(p.q) +
@@ -252,7 +245,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                     qb[2 * w][1] = f1;
                     qb[2 * w + 1][0] = f2;
                     qb[2 * w + 1][1] = f3;
-                } else if (slot == 0) {
+                } else if (warp == 0) {
                     s_q[((2 * w) * NT + nt) * 32 + lane] = make_uint2(f0, f1);
                     s_q[((2 * w + 1) * NT + nt) * 32 + lane] = make_uint2(f2, f3);
                 }
@@ -371,7 +364,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         // last visible position of the column (those past R see nothing)
-                        const int n = r_base + nt * 8 + 2 * t4 + c;
+                        const int n = nt * 8 + 2 * t4 + c;
                         const int limit = n < R ? first_limit + n / G : -1;
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
@@ -482,17 +475,15 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
             copy_next();
             cp_async_wait<kStages - 1>();
             __syncwarp();
-            const int j0 = (cc.t + it) * p.tile + slot * kPos;
+            const int j0 = (cc.t + it) * kTile + warp * kPos;
             const uint8_t *st = ring_p + (done % kStages) * C::kStageBytes;
-            if (r_base < R) {
-                if (j0 + kPos - 1 <= first_limit)
-                    step(st, j0, std::false_type{});
-                else if (j0 < kv_len)  // (a second page past the end is masked as a whole)
-                    step(st, j0, std::true_type{});
-            }
+            if (j0 + kPos - 1 <= first_limit)
+                step(st, j0, std::false_type{});
+            else if (j0 < kv_len)  // (a second page past the end is masked as a whole)
+                step(st, j0, std::true_type{});
             __syncwarp();  // (the stage's next copies)
         }
-        // ---- end of the share: merge the slots ----
+        // ---- end of the share: merge the warps ----
         float l[NT][2], cr[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -513,9 +504,9 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
         }
         float *part = reinterpret_cast<float *>(smem + C::kRing);
 #pragma unroll 1
-        for (int half = slots / 2; half > 0; half >>= 1) {
-            if (slot >= half && slot < 2 * half) {
-                float *d = part + (warp - half * blocks) * C::kPart + lane;
+        for (int half = kWarps / 2; half > 0; half >>= 1) {
+            if (warp >= half && warp < 2 * half) {
+                float *d = part + (warp - half) * C::kPart + lane;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -531,7 +522,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                 }
             }
             __syncthreads();
-            if (slot < half) {
+            if (warp < half) {
                 const float *d = part + warp * C::kPart + lane;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -561,12 +552,12 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
             if (starts) uc[0] = blockIdx.x;
             if (ends) uc[1] = blockIdx.x;
         }
-        if (slot == 0) {
+        if (warp == 0) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int n = r_base + nt * 8 + 2 * t4 + c;
+                    const int n = nt * 8 + 2 * t4 + c;
                     if (n >= R) continue;
                     // this lane's channels [D/8 g, D/8 (g + 1)) of column n, in order
                     float x[D / 8];
@@ -602,8 +593,6 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                     }
                 }
         }
-        // (one slot: nothing above keeps the next share's query fragments off this one's readers)
-        if (!kQRegs && slots == 1) __syncthreads();
         cc.skip(p, n_seg);
     }
     cp_async_wait<0>();
@@ -618,23 +607,22 @@ cudaError_t launch_t(const Kv4Params &p, cudaStream_t s) {
     return e != cudaSuccess || p.whole ? e : launch_kv4_merge(p, s);
 }
 
-int row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
-
 template <int D>
 cudaError_t launch_d(const Kv4Params &p, cudaStream_t s) {
-    const int nt = row_tiles(p.group * p.max_q_rows);
-    return nt == 1 ? launch_t<D, 1>(p, s) : nt == 2 ? launch_t<D, 2>(p, s) : launch_t<D, 4>(p, s);
+    return p.group * p.max_q_rows <= 8 ? launch_t<D, 1>(p, s) : launch_t<D, 2>(p, s);
 }
 
 }  // namespace
 
+// From 17 rows on the tcgen05 kernel is faster (28 sequences of 26,027 positions, 4 KV heads: this
+// kernel with 32 rows per warp took 228 us for 21 rows and 230 for 28, the tcgen05 one 216 and 219;
+// one sequence of 8,710 and 28 rows 24.1 against 22.7).  Up to 16 this one is: 187 against 210 us
+// for 14 rows, 15.1 against 16.8 for the one sequence.
 int kv4_mma_max_rows() { return 16; }
 
-// Row blocks of 32 rows (1, 2 or 4 of them) leave 8, 4 or 2 slots of 32 positions to a tile.
-void kv4_mma_plan(int head_dim, int rows, int *tile, int *per_sm) {
-    (void)head_dim;
-    *tile = kPos * (rows <= 32 ? kWarps : rows <= 64 ? kWarps / 2 : kWarps / 4);
-    *per_sm = ctas_per_sm(row_tiles(rows));
+void kv4_mma_plan(int *tile, int *per_sm) {
+    *tile = kTile;
+    *per_sm = kCtasPerSm;
 }
 
 cudaError_t launch_kv4_mma(const Kv4Params &p, cudaStream_t s) {

@@ -480,33 +480,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             const uint4 *src = reinterpret_cast<const uint4 *>(
                 static_cast<const unsigned short *>(p.q) +
                 ((int64_t)(u.q0 + (has ? r / G : 0)) * p.h_q + u.g * G + (has ? r % G : 0)) * D);
-            auto load = [&](int c, float (&f)[8]) {
-                Chunk<true>::to_float(has ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u), f);
-            };
-            float top = 0.f;
-            qsum = 0.f;
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-                float f[8];
-                load(c, f);
+            auto load = [&](int c) { return has ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u); };
+            uint32_t top = 0;  // largest magnitudes of both halves, as bits
+            float2 sum = make_float2(0.f, 0.f);
+            uint4 x[D / 8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    qsum += f[e];
-                    top = fmaxf(top, fabsf(f[e]));
+            for (int c = 0; c < D / 8; ++c) x[c] = load(c);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    top = __vmaxu2(top, w[e] & 0x7fff7fffu);
+                    sum = __fadd2_rn(sum, make_float2(__uint_as_float(w[e] << 16),
+                                                      __uint_as_float(w[e] & 0xffff0000u)));
                 }
             }
-            const float scale = query_scale(top, unscale);
-#pragma unroll 1
+            qsum = sum.x + sum.y;
+            const float scale =
+                query_scale(__uint_as_float(max(top << 16, top & 0xffff0000u)), unscale);
+            // (channel 2 i is a word's low half; odd channels' codes are 16 times as large)
+            const float2 by = make_float2(scale, scale * 0.0625f);
+#pragma unroll 
             for (int c = 0; c < D / 8; c += 4) {
                 uint32_t q[16];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float f[8];
-                    load(c + i, f);
+                    const uint4 y = x[c + i];
+                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                    float2 f[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] *= e & 1 ? scale * 0.0625f : scale;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) q[4 * i + e] = pack_f16(f[e], f[e + 4]);
+                    for (int e = 0; e < 4; ++e)
+                        f[e] = __fmul2_rn(make_float2(__uint_as_float(w[e] << 16),
+                                                      __uint_as_float(w[e] & 0xffff0000u)),
+                                          by);
+                    q[4 * i] = pack_f16(f[0].x, f[2].x);
+                    q[4 * i + 1] = pack_f16(f[0].y, f[2].y);
+                    q[4 * i + 2] = pack_f16(f[1].x, f[3].x);
+                    q[4 * i + 3] = pack_f16(f[1].y, f[3].y);
                 }
                 tmem_st16(lane_base + kColQ + c * 4, q);
             }

@@ -251,7 +251,7 @@ struct Kv4Params {
 int kv4_simt_splits(int batch, int h_kv, int rows, int max_kv_len);
 cudaError_t launch_kv4_simt(const Kv4Params &p, cudaStream_t s);
 int kv4_mma_max_rows();  // rows per KV head of the register-expanding tensor-core engine
-void kv4_mma_plan(int head_dim, int rows, int *tile, int *ctas_per_sm);
+void kv4_mma_plan(int *tile, int *ctas_per_sm);
 cudaError_t launch_kv4_mma(const Kv4Params &p, cudaStream_t s);
 int kv4_tc_max_rows();  // rows per KV head of the tcgen05 engine
 void kv4_tc_plan(int *tile, int *ctas_per_sm);

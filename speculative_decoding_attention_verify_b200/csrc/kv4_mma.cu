@@ -12,8 +12,8 @@
 // channels, whose codes sit in bits 4-7, by 1/16.  For the values
 //     sum_j p_j v_j = sum_j (p_j s_j) c_j + sum_j p_j lo_j
 // with w_j = p_j s_j taken as one exponential, w_j = 2^(x_j + log2 s_j - m), x_j the score in log2
-// units and m a running maximum of the whole exponent.  w is rounded to fp16 (2^-12 of itself, and
-// the largest w is between 1 and 2^14) and p = w / s is not rounded: it enters the sums of the
+// units and m a running maximum of the whole exponent.  w is rounded to fp16 (2^-12 of itself; see
+// kTopLog2 for the smallest ones) and p = w / s is not rounded: it enters the sums of the
 // softmax and of p lo in fp32.  Rows of one value (s = 0, codes 0) count with s = 1 there.
 //
 // Layout.  Everything is transposed: S^T = K Q^T and O^T = V^T P^T by mma.sync m16n8k16 with 16
@@ -31,8 +31,8 @@
 // warps takes 32 positions (two pages) for all rows.  Each warp streams its positions through its
 // own two cp.async stages, with its page numbers looked up a stage further ahead, and keeps its own
 // running maxima, sums and O^T; there is no block-wide step until a unit ends, where the warps'
-// shares are merged pairwise through shared memory.  The maximum moves only when a score exceeds
-// it by more than 2^14 (one vote per 32 positions; a weight stays finite in fp16).
+// shares are merged pairwise through shared memory.  Whether a maximum moves is one vote per 32
+// positions.
 // Query fragments are registers for up to 8 rows; for more they are read from shared memory, once
 // for both pages.
 #include <type_traits>
@@ -51,7 +51,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kPos = 32;       // positions of a warp per tile
 constexpr int kStages = 2;
-constexpr float kGrow = 14.0f;  // weights stay below fp16's largest number
 
 constexpr int kTile = kWarps * kPos;
 constexpr int kCtasPerSm = 2;  // registers of O^T decide
@@ -380,7 +379,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                 for (int c = 0; c < 2; ++c)
                     grow |= fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]),
                                   fmaxf(s[1][nt][c], s[1][nt][2 + c])) >
-                            (m[nt][c] == -INFINITY ? -INFINITY : kGrow);
+                            (m[nt][c] == -INFINITY ? -INFINITY : kGrowLog2);
             if (__any_sync(FULL, grow)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -392,7 +391,8 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                         x = fmaxf(x, __shfl_xor_sync(FULL, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(FULL, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(FULL, x, 16));
-                        const bool up = x > (m[nt][c] == -INFINITY ? -INFINITY : kGrow);
+                        const bool up = x > (m[nt][c] == -INFINITY ? -INFINITY : kGrowLog2);
+                        x -= kTopLog2;
                         f[c] = up && m[nt][c] != -INFINITY ? ex2(-x) : 1.f;
                         if (up) {
                             m[nt][c] = (m[nt][c] == -INFINITY ? 0.f : m[nt][c]) + x;

@@ -22,14 +22,20 @@
 // 0 4 1 5 2 6 3 7; Q is written to TMEM in the same order and O's columns are read back in it, so
 // no code is ever moved to its own place.
 // The softmax takes 32 columns at a time in one pass: the exponents are taken from the running
-// maximum as it stands, and only when one exceeds it by more than 2^14 does the maximum move
-// (then O, the sums and the tile's earlier weights are rescaled).  A second pass, or a tile's columns unrolled into one block of code, costs more
-// than its instructions: the warps' roles together must stay within the instruction cache (with
-// 64 columns and 32 positions unrolled, two of three issue slots were lost to instruction fetch
-// and a tile took 7,000 cycles).
+// maximum as it stands, and only when one exceeds kGrowLog2 does the maximum move (then O, the sums
+// and the tile's earlier weights are rescaled).  A second pass, or more columns unrolled into one
+// block of code, costs more than its instructions: the warps' roles together must stay within
+// the instruction cache (with 64 columns and 32 positions unrolled, two of three issue slots were
+// lost to instruction fetch and a tile took 7,000 cycles).
 // K and V tiles, S and P are double-buffered: S of tile t overwrites the buffer of tile t - 2
-// once that tile's P V has completed.  Bound by the SM's issue slots and shared memory: a tile's
-// 16 KB of codes become 64 KB written and read again by the tensor core.
+// once that tile's P V has completed.
+// Bound by the chain of those steps: with two buffers (TMEM has no room for a third beside O and Q)
+// a tile's S, its softmax and its P V follow one another, 2,400 cycles a tile for 63 rows and 128
+// channels, of which the softmax has 1,800; the tensor core is busy for 29% of them, issue slots
+// 38%, shared memory 39%, HBM 20%.  28 sequences of 26,033 positions, 4 KV heads: 244 us, 1.6 TB/s.
+// What that cost on the way: bf16 codes and weights with eight expanding warps 277 us; every
+// expanding warp with its own cp.async ring instead of a copying warp 269; the positions' factors
+// loaded where they are used 274; 64 columns at a time 293.
 // Every wait on an mbarrier is bounded (see sd_set_wait_timeout_ns); on expiry the CTA records
 // SD_DEVERR_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
 #include <type_traits>
@@ -57,7 +63,6 @@ constexpr int kStages = 4;           // ring of tiles in flight
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;      // S / P buffers at 0 and 128
 constexpr uint32_t kColQ = 384;
-constexpr float kRescaleLog2 = 14.0f;  // weights stay below fp16's largest number
 constexpr uint32_t kHalfBytes = kTile * 128;  // 64 channels of a tile
 constexpr int kParSlots = 4;         // tiles whose position factors are kept:
 // pairs of positions' (s, lo) of K [0, 256), log2 s of V [256, 384), (1 / s, lo / s) [384, 640)
@@ -633,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                             mx[k] = max3(mx[k], v[k >> 1][4 * i + 2 * (k & 1)],
                                          v[k >> 1][4 * i + 2 * (k & 1) + 1]);
                         // (before a row's first visible position its maximum is -inf and nm is 0)
-                        grow |= mx[k] > (mk[k] == -INFINITY ? -INFINITY : kRescaleLog2);
+                        grow |= mx[k] > (mk[k] == -INFINITY ? -INFINITY : kGrowLog2);
                     }
                     if (__any_sync(FULL, grow)) {
                         float f[4];
@@ -641,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                         for (int k = 0; k < 4; ++k) {
                             float x = fmaxf(mx[k], __shfl_xor_sync(FULL, mx[k], 1));
                             x = fmaxf(x, __shfl_xor_sync(FULL, x, 2));
-                            const bool up = x > (mk[k] == -INFINITY ? -INFINITY : kRescaleLog2);
+                            const bool up = x > (mk[k] == -INFINITY ? -INFINITY : kGrowLog2);
+                            x -= kTopLog2;
                             f[k] = up && mk[k] != -INFINITY ? ex2(-x) : 1.f;
                             if (up) {
                                 mk[k] = x - nm[k];

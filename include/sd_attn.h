@@ -587,10 +587,14 @@ SD_API sd_status sd_kv4_attention_workspace_size(const sd_q_desc *q, const sd_kv
  * Dense attention over a 4-bit cache: what sd_verify_attention computes, with the values that
  * the cache's rows stand for as K and V.  One row per sequence is plain decoding.  q_data and
  * out hold kv->dtype.  Neither K nor V is ever dequantised in memory: scores are formed on the
- * codes themselves (exact in bf16) and corrected by each row's s and lo, and V's scale is folded
- * into the softmax weights.  bf16 rows run on tensor cores (up to 128 rows per KV head, q_data
- * and out 16-byte aligned), the rest on CUDA cores.  workspace: 16-byte aligned, not shared
- * with a call in flight.  A sequence whose hints are violated (more than max_q_rows rows, kv_len
+ * codes themselves (exact in fp16) and corrected by each row's s and lo, and V's scale is folded
+ * into the softmax weights, which are rounded to fp16 (half a step: 2^-11 of a weight, or 2^-35
+ * of its row's largest) where they multiply the codes and nowhere else; everything else is fp32.
+ * A row of V whose s lies between 0 and 2^-90 counts with s = 2^-90.  bf16 rows run on tensor
+ * cores (up to 128 rows per KV head, q_data and out 16-byte aligned), the rest, without that
+ * rounding and lower bound, on CUDA cores.  The kernel for 17 to 128 rows waits with the bound of
+ * sd_set_wait_timeout_ns (SD_DEVERR_TIMEOUT).  workspace: 16-byte aligned, not shared with a call
+ * in flight.  A sequence whose hints are violated (more than max_q_rows rows, kv_len
  * below its rows or above max_kv_len or its pages) sets SD_DEVERR_SHAPE and its rows of out are
  * left as they were; rows on a page outside the pool (SD_DEVERR_PAGE) count as zeros.
  */

@@ -79,6 +79,16 @@ __device__ __forceinline__ uint32_t codes_at(uint32_t w, uint32_t w8) {
     return (P < 2 ? w : w8) & (P & 1 ? 0x00f000f0u : 0x000f000fu);
 }
 
+// The same codes as whole numbers around zero: c - 8 (P even) or 16 (c - 8) (P odd), from the
+// fp16 numbers 1024 + c and 1024 + 16 c.
+template <int P>
+__device__ __forceinline__ uint32_t centred_at(uint32_t w, uint32_t w8) {
+    const uint32_t x = codes_at<P>(w, w8) | 0x64006400u;
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&x),
+                              __float2half2_rn(P & 1 ? 1152.f : 1032.f));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 p = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
@@ -96,7 +106,8 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-// Power of two that brings a row's largest query element below 2^14, and 2^24 over it.
+// Power of two that brings a row's largest query element below 2^14, and 2^24 over it (codes_at's
+// scale).
 __device__ __forceinline__ float query_scale(float top, float &unscale) {
     const int e = (int)(__float_as_uint(top) >> 23);  // biased; 255: not finite
     // (rows of zeros, and elements beyond 2^114 or not finite, keep a scale that is in range)

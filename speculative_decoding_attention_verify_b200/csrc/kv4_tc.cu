@@ -1,8 +1,12 @@
 // tcgen05 attention over a 4-bit cache for many rows per KV head (verification): 17 to 128 rows,
 // bf16.
 //
-// The mathematics is kv4_mma.cu's: codes are fp16 numbers as they stand, the queries are scaled
-// per row, and V's scale is in the weights' exponent.  With this many rows the products outgrow
+// The mathematics is kv4_mma.cu's: the codes themselves are multiplied, the queries are scaled per
+// row, and V's scale is in the weights' exponent.  A code is c - 8 here, one more instruction per
+// pair than c 2^-24: one accumulator gathers hundreds of tiles, its sum of w c would be far larger
+// than the output that is left after lo's part is added, and the tensor core rounds towards zero
+// as it accumulates (26,033 random positions: output off by 5e-3 of itself with c, 2e-3, most of
+// it the output's own rounding, with c - 8).  With this many rows the products outgrow
 // mma.sync (1,024 products per cycle per SM; a tile of 64 rows would need 2,048 cycles, three times
 // what it takes from HBM), so the codes are spread to fp16 tiles in shared memory once and used by
 // tcgen05.mma (4,096 products per cycle).
@@ -18,7 +22,7 @@
 //   warp 8     S = Q K^T issuer (Q from TMEM), TMEM owner
 //   warp 9     O += P V issuer (P from TMEM)
 //   warp 10    copies tiles up to kStages ahead: one bulk copy per page for the codes of K and of V
-// A word of 8 codes becomes one 16-byte chunk by 4 ANDs and a shift, its channels in the order
+// A word of 8 codes becomes one 16-byte chunk by 4 logic operations, 4 additions and a shift, its channels in the order
 // 0 4 1 5 2 6 3 7; Q is written to TMEM in the same order and O's columns are read back in it, so
 // no code is ever moved to its own place.
 // The softmax takes 32 columns at a time in one pass: the exponents are taken from the running
@@ -254,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
     auto wait1 = [&](int bar, int parity) {
         bool ok = true;
         if (lane == 0) ok = wait(bar, parity);
+        __syncwarp();  // (orders what lane 0 has seen before the other lanes' accesses)
         return __shfl_sync(FULL, ok ? 1 : 0, 0) != 0;
     };
 
@@ -286,8 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                     // (32 / Q rows on; the swizzle of row r is r mod 8, and 32 / Q is 8 or 16)
                     *reinterpret_cast<uint4 *>(dst + i * (32 / Q) * 128 +
                                                (at ^ (uint32_t)(c << 4))) =
-                        make_uint4(codes_at<0>(w[c], w8), codes_at<1>(w[c], w8),
-                                   codes_at<2>(w[c], w8), codes_at<3>(w[c], w8));
+                        make_uint4(centred_at<0>(w[c], w8), centred_at<1>(w[c], w8),
+                                   centred_at<2>(w[c], w8), centred_at<3>(w[c], w8));
                 }
             }
             fence_async_smem();
@@ -312,14 +317,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                     const uint32_t wk = w[0], wv = w[kTile];
                     float *f = s_par + (t % kParSlots) * kParFloats;
                     float *d = f + (j >> 1) * 4 + (j & 1);
-                    d[0] = param_scale(wk) * p.scale_log2;
-                    d[2] = param_low(wk) * p.scale_log2;
+                    // (a code stands here for c - 8: lo moves by 8 s)
+                    const float sk = param_scale(wk);
+                    d[0] = sk * p.scale_log2;
+                    d[2] = fmaf(8.f, sk, param_low(wk)) * p.scale_log2;
+                    // (rows of one value have codes 0; any s serves, and one well below lo lets
+                    // -8 and + 8 cancel to 2^-17 of lo)
                     float sc = param_scale(wv);
-                    sc = sc == 0.f ? 1.f : fmaxf(sc, kMinScale);
+                    sc = fmaxf(sc == 0.f ? fabsf(param_low(wv)) * 0.00390625f : sc, kMinScale);
                     const float inv = rcp(sc);
                     f[2 * kTile + j] = lg2(sc);
                     d[3 * kTile] = inv;
-                    d[3 * kTile + 2] = param_low(wv) * inv;
+                    d[3 * kTile + 2] = fmaf(param_low(wv), inv, 8.f);
                 }
                 expand(st + v * C::kCodes, (v ? sV : sK) + s * C::kTileBytes);
                 if (lane == 0) mbar_arrive(BAR((v ? VF : KF) + s));
@@ -479,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
         float4 *s_o = reinterpret_cast<float4 *>(s_l + kRows);  // [copy - 1][RPC][8]
         // Q of unit u into TMEM (zeros past its rows), channels of each group of 8 in the order of
         // the spread codes.
-        float qsum, unscale;  // of this lane's row: sum of the query, 2^24 / its scale
+        float qsum, unscale;  // of this lane's row: sum of the query, 1 / its scale
         auto write_q = [&](const Kv4Cursor &u) {
             const bool has = r < u.n_q * G;
             const uint4 *src = reinterpret_cast<const uint4 *>(
@@ -504,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             qsum = sum.x + sum.y;
             const float scale =
                 query_scale(__uint_as_float(max(top << 16, top & 0xffff0000u)), unscale);
+            unscale *= 0x1p-24f;  // (codes are whole numbers here)
             // (channel 2 i is a word's low half; odd channels' codes are 16 times as large)
             const float2 by = make_float2(scale, scale * 0.0625f);
 #pragma unroll 
@@ -798,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                 if (read_o) tmem_ld32(lane_base + kColO + c * 32, o);
 #pragma unroll
                 for (int e = 0; e < 32; ++e)  // (codes of odd channels were 16 times as large)
-                    o[e] = fmaf(o[e], e & 2 ? 1048576.f : 16777216.f, cr);
+                    o[e] = fmaf(o[e], e & 2 ? 0.0625f : 1.f, cr);
                 if constexpr (NCP > 1) {
                     // copies 1.. pass their 32 columns through shared memory (16-byte chunk k of
                     // row r in slot k ^ (r & 7))

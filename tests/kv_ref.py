@@ -162,7 +162,10 @@ def attention_bound(q, cache, i, dtype, scale=None):
     score's error is below scale * sum|q_e| * (15 s + |lo|) * 2^-20 (128 products of at most 15
     steps, each a few 2^-24 of the running sum), which moves every weight by that much relative to
     itself; 2^-18 covers the sums of weights, their exponentials and logarithms, and the merges.
-    Both act on the codes' part s c and the low values' part of a value separately."""
+    Both act on the codes' part s c and the low values' part of a value separately.  The kernel for
+    many rows multiplies c - 8 instead of c and adds 8 s to lo, so the larger of c and |c - 8| (at
+    most 15 as before) bounds what a rounded weight multiplies; for a row of one value (s = 0) it
+    counts s = 2^-8 |lo| with the code -8, whose rounding is 2^-11 8 2^-8 |lo| = 2^-16 |lo|."""
     k, v = cache.kv[i]
     n, h_q, d = q.shape
     g = h_q // cache.h_kv
@@ -172,9 +175,11 @@ def attention_bound(q, cache, i, dtype, scale=None):
     step = kp[..., 0].double().abs() * 15 + kp[..., 1].double().abs()
     worst = step.amax(-1).repeat_interleave(g, 0)[None, :, None]
     err = sc * q.double().abs().sum(-1, keepdim=True) * worst * 2.0 ** -20 + 2.0 ** -18
-    codes = attention(q, k, (vp[..., :1].double() * vc.double()).abs(), scale)
-    parts = codes + attention(q, k, vp[..., 1:].double().abs().expand_as(v), scale)
+    most = torch.maximum(vc.double(), (vc.double() - 8).abs())
+    codes = attention(q, k, (vp[..., :1].double() * most).abs(), scale)
+    lows = attention(q, k, vp[..., 1:].double().abs().expand_as(v), scale)
+    parts = codes + lows
     bound = 2 * err * parts + HALF_STEP[dtype] * out.abs()
     if dtype == torch.bfloat16:
-        bound = bound + 2.0 ** -11 * codes
+        bound = bound + 2.0 ** -11 * codes + 2.0 ** -16 * lows
     return out, bound

@@ -17,11 +17,11 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("gap", [20.0, 24.5, 28.5, 32.0])
 @pytest.mark.parametrize("rows", [1, 3, 9])
 def test_many_positions_of_next_to_no_weight(rows, gap, paged):
-    """One position `gap` powers of two above 30,000 others, with values of zero: the output is
-    what the others leave.  A weight is rounded to fp16 below a largest weight of 2^10 or more, so
+    """One position `gap` powers of two above 30,000 others, whose codes are zero (its values too): the
+    output is what the others leave.  A weight is rounded to fp16 below a largest weight of 2^10 or more, so
     it is off by half a step, 2^-11 of itself, or by half of 2^-24, 2^-35 of the row's largest: over
-    all positions 2^-11 sum p s c + 2^-35 max(p s) sum c on top of attention_bound's other terms.
-    (A row of zeros is stored with s = 0 and counts with s = 1.)"""
+    all positions 2^-11 sum p s c + 2^-35 max(p s) sum max(c, |c - 8|) on top of
+    attention_bound's other terms."""
     h_q, h_kv, d, length = 7, 1, 128, 30000
     c = Call([length], [rows], h_q, h_kv, d, paged, seed=rows)
     # keys: position 5 all ones, the others zeros (s = 0, lo = the value); queries of one sum
@@ -34,7 +34,6 @@ def test_many_positions_of_next_to_no_weight(rows, gap, paged):
             codes[:] = (torch.arange(length)[:, None] + torch.arange(d)[None]) % 15 + 1
             param[..., 0] = 1.0
             codes[:, 5] = 0
-            param[:, 5] = 0
         c.cache.store(w, 0, R.pack(codes), param)
         c.cache.parts[0][w] = (codes, param)
         c.cache.kv[0][w] = R.values(R.pack(codes), param)
@@ -47,8 +46,8 @@ def test_many_positions_of_next_to_no_weight(rows, gap, paged):
     assert flag == 0
     ref, bound = R.attention_bound(q, c.cache, 0, BF, soft)
     vc = c.cache.parts[0][1][0].double()
-    # p s is largest at position 5 (s counts as 1 there): p < 1
-    bound = bound + 2.0 ** -35 * vc.sum(1)[:, None].expand(1, h_q, d).reshape(1, h_q, d)
+    # p s is largest at position 5, where p < 1 and s = 1
+    bound = bound + 2.0 ** -35 * torch.maximum(vc, (vc - 8).abs()).sum(1)[:, None].expand(1, h_q, d).reshape(1, h_q, d)
     assert ((out.double() - ref).abs() <= bound).all(), ((out.double() - ref).abs() / bound).max()
 
 

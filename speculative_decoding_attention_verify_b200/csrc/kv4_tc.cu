@@ -2,8 +2,8 @@
 // bf16.
 //
 // The mathematics is kv4_mma.cu's: the codes themselves are multiplied, the queries are scaled per
-// row, and V's scale is in the weights' exponent.  A code is c - 8 here, one more instruction per
-// pair than c 2^-24: one accumulator gathers hundreds of tiles, its sum of w c would be far larger
+// row, and V's scale is in the weights' exponent.  V's codes are c - 8 here, one more instruction
+// per pair than c 2^-24: one accumulator gathers hundreds of tiles, its sum of w c would be far larger
 // than the output that is left after lo's part is added, and the tensor core rounds towards zero
 // as it accumulates (26,033 random positions: output off by 5e-3 of itself with c, 2e-3, most of
 // it the output's own rounding, with c - 8).  With this many rows the products outgrow
@@ -22,7 +22,7 @@
 //   warp 8     S = Q K^T issuer (Q from TMEM), TMEM owner
 //   warp 9     O += P V issuer (P from TMEM)
 //   warp 10    copies tiles up to kStages ahead: one bulk copy per page for the codes of K and of V
-// A word of 8 codes becomes one 16-byte chunk by 4 logic operations, 4 additions and a shift, its channels in the order
+// A word of 8 codes becomes one 16-byte chunk by 4 logic operations and a shift (V: and 4 additions), its channels in the order
 // 0 4 1 5 2 6 3 7; Q is written to TMEM in the same order and O's columns are read back in it, so
 // no code is ever moved to its own place.
 // The softmax takes 32 columns at a time in one pass: the exponents are taken from the running
@@ -36,10 +36,11 @@
 // Bound by the chain of those steps: with two buffers (TMEM has no room for a third beside O and Q)
 // a tile's S, its softmax and its P V follow one another, 2,400 cycles a tile for 63 rows and 128
 // channels, of which the softmax has 1,800; the tensor core is busy for 29% of them, issue slots
-// 38%, shared memory 39%, HBM 20%.  28 sequences of 26,033 positions, 4 KV heads: 244 us, 1.6 TB/s.
-// What that cost on the way: bf16 codes and weights with eight expanding warps 277 us; every
-// expanding warp with its own cp.async ring instead of a copying warp 269; the positions' factors
-// loaded where they are used 274; 64 columns at a time 293.
+// 38%, shared memory 39%, HBM 20%. 28 sequences of 26,033 positions, 4 KV heads, 63 rows: 261 us, 1.5 TB/s.
+// Measured on the way, with codes not yet centred (then 250 us): every expanding warp with its own
+// cp.async ring instead of a copying warp 269; the positions' factors loaded where they are used
+// 274; 64 columns at a time 293.  Centred: one code for K's and V's expansion 274, the four steps of
+// an expansion unrolled together 275.
 // Every wait on an mbarrier is bounded (see sd_set_wait_timeout_ns); on expiry the CTA records
 // SD_DEVERR_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
 #include <type_traits>
@@ -275,24 +276,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
         const bool swap = eq >= 2;
         const uint32_t at = (uint32_t)((ew * kWarpRows + er) * 128) + (uint32_t)(eq >> 1) * kHalfBytes +
                             (uint32_t)((((eq & 1) * 4) ^ (swap ? 2 : 0) ^ (er & 7)) << 4);
-        auto expand = [&](const uint8_t *src, uint8_t *dst) {
-            uint4 x[kLoads];
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                x[i] = *reinterpret_cast<const uint4 *>(src + ew * kWarpRows * C::kRow + i * 512 +
-                                                        lane * 16);
-#pragma unroll
+        auto expand = [&](const uint8_t *src, uint8_t *dst, auto is_v) {
+            constexpr bool kV = decltype(is_v)::value;
+#pragma unroll 2
             for (int i = 0; i < kLoads; ++i) {
-                const uint32_t w[4] = {swap ? x[i].z : x[i].x, swap ? x[i].w : x[i].y,
-                                       swap ? x[i].x : x[i].z, swap ? x[i].y : x[i].w};
+                const uint4 x = *reinterpret_cast<const uint4 *>(
+                    src + ew * kWarpRows * C::kRow + i * 512 + lane * 16);
+                const uint32_t w[4] = {swap ? x.z : x.x, swap ? x.w : x.y,
+                                       swap ? x.x : x.z, swap ? x.y : x.w};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const uint32_t w8 = w[c] >> 8;
                     // (32 / Q rows on; the swizzle of row r is r mod 8, and 32 / Q is 8 or 16)
                     *reinterpret_cast<uint4 *>(dst + i * (32 / Q) * 128 +
                                                (at ^ (uint32_t)(c << 4))) =
-                        make_uint4(centred_at<0>(w[c], w8), centred_at<1>(w[c], w8),
-                                   centred_at<2>(w[c], w8), centred_at<3>(w[c], w8));
+                        kV ? make_uint4(centred_at<0>(w[c], w8), centred_at<1>(w[c], w8),
+                                        centred_at<2>(w[c], w8), centred_at<3>(w[c], w8))
+                           : make_uint4(codes_at<0>(w[c], w8), codes_at<1>(w[c], w8),
+                                        codes_at<2>(w[c], w8), codes_at<3>(w[c], w8));
                 }
             }
             fence_async_smem();
@@ -303,38 +304,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             const int s = t & 1;
             const uint8_t *st = smem + C::kRing + (t % kStages) * C::kStageBytes;
             if (!wait1(RF + t % kStages, t / kStages)) break;
-            bool ok = true;
-#pragma unroll 1
-            for (int v = 0; v < 2; ++v) {  // K, then V (one copy of the code)
-                ok = t < 2 || wait1((v ? PD : KE) + s, (t - 2) >> 1);
-                if (!ok) break;
-                if (v == 0) {
-                    // Factors of the positions.  (Slot t % 4: the softmax of tile t - 4 is past it,
-                    // since S of tile t - 2 has completed and that waited for the P V of tile
-                    // t - 4.)
-                    const int j = ew * kWarpRows + lane;
-                    const uint32_t *w = reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes) + j;
-                    const uint32_t wk = w[0], wv = w[kTile];
-                    float *f = s_par + (t % kParSlots) * kParFloats;
-                    float *d = f + (j >> 1) * 4 + (j & 1);
-                    // (a code stands here for c - 8: lo moves by 8 s)
-                    const float sk = param_scale(wk);
-                    d[0] = sk * p.scale_log2;
-                    d[2] = fmaf(8.f, sk, param_low(wk)) * p.scale_log2;
-                    // (rows of one value have codes 0; any s serves, and one well below lo lets
-                    // -8 and + 8 cancel to 2^-17 of lo)
-                    float sc = param_scale(wv);
-                    sc = fmaxf(sc == 0.f ? fabsf(param_low(wv)) * 0.00390625f : sc, kMinScale);
-                    const float inv = rcp(sc);
-                    f[2 * kTile + j] = lg2(sc);
-                    d[3 * kTile] = inv;
-                    d[3 * kTile + 2] = fmaf(param_low(wv), inv, 8.f);
-                }
-                expand(st + v * C::kCodes, (v ? sV : sK) + s * C::kTileBytes);
-                if (lane == 0) mbar_arrive(BAR((v ? VF : KF) + s));
+            if (t >= 2 && !wait1(KE + s, (t - 2) >> 1)) break;
+            {
+                // Factors of the positions.  (Slot t % 4: the softmax of tile t - 4 is past it,
+                // since S of tile t - 2 has completed and that waited for the P V of tile t - 4.)
+                const int j = ew * kWarpRows + lane;
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes) + j;
+                const uint32_t wk = w[0], wv = w[kTile];
+                float *f = s_par + (t % kParSlots) * kParFloats;
+                float *d = f + (j >> 1) * 4 + (j & 1);
+                d[0] = param_scale(wk) * p.scale_log2;
+                d[2] = param_low(wk) * p.scale_log2;
+                // (a V code stands for c - 8: lo moves by 8 s.  Rows of one value have codes 0; any
+                // s serves, and one well below lo lets -8 and + 8 cancel to 2^-17 of lo)
+                float sc = param_scale(wv);
+                sc = fmaxf(sc == 0.f ? fabsf(param_low(wv)) * 0.00390625f : sc, kMinScale);
+                const float inv = rcp(sc);
+                f[2 * kTile + j] = lg2(sc);
+                d[3 * kTile] = inv;
+                d[3 * kTile + 2] = fmaf(param_low(wv), inv, 8.f);
             }
-            if (!ok) break;
-            if (lane == 0) mbar_arrive(BAR(RE + t % kStages));
+            expand(st, sK + s * C::kTileBytes, std::false_type{});
+            if (lane == 0) mbar_arrive(BAR(KF + s));
+            if (t >= 2 && !wait1(PD + s, (t - 2) >> 1)) break;
+            expand(st + C::kCodes, sV + s * C::kTileBytes, std::true_type{});
+            if (lane == 0) {
+                mbar_arrive(BAR(VF + s));
+                mbar_arrive(BAR(RE + t % kStages));
+            }
         }
     } else if (warp == kCopyWarp) {
         // ---------------------------------------------------------- copy ----------------------
@@ -488,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
         float4 *s_o = reinterpret_cast<float4 *>(s_l + kRows);  // [copy - 1][RPC][8]
         // Q of unit u into TMEM (zeros past its rows), channels of each group of 8 in the order of
         // the spread codes.
-        float qsum, unscale;  // of this lane's row: sum of the query, 1 / its scale
+        float qsum, unscale;  // of this lane's row: sum of the query, 2^24 / its scale
         auto write_q = [&](const Kv4Cursor &u) {
             const bool has = r < u.n_q * G;
             const uint4 *src = reinterpret_cast<const uint4 *>(
@@ -513,7 +510,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             qsum = sum.x + sum.y;
             const float scale =
                 query_scale(__uint_as_float(max(top << 16, top & 0xffff0000u)), unscale);
-            unscale *= 0x1p-24f;  // (codes are whole numbers here)
             // (channel 2 i is a word's low half; odd channels' codes are 16 times as large)
             const float2 by = make_float2(scale, scale * 0.0625f);
 #pragma unroll 

@@ -34,13 +34,13 @@
 // K and V tiles, S and P are double-buffered: S of tile t overwrites the buffer of tile t - 2
 // once that tile's P V has completed.
 // Bound by the chain of those steps: with two buffers (TMEM has no room for a third beside O and Q)
-// a tile's S, its softmax and its P V follow one another, 2,400 cycles a tile for 63 rows and 128
-// channels, of which the softmax has 1,800; the tensor core is busy for 29% of them, issue slots
-// 38%, shared memory 39%, HBM 20%. 28 sequences of 26,033 positions, 4 KV heads, 63 rows: 261 us, 1.5 TB/s.
-// Measured on the way, with codes not yet centred (then 250 us): every expanding warp with its own
-// cp.async ring instead of a copying warp 269; the positions' factors loaded where they are used
-// 274; 64 columns at a time 293.  Centred: one code for K's and V's expansion 274, the four steps of
-// an expansion unrolled together 275.
+// a tile's S, its softmax and its P V follow one another, about 2,600 cycles a tile for 63 rows and
+// 128 channels, of which the softmax has 2,200; the tensor core is busy for 29% of the kernel's
+// time, issue slots for 38%, shared memory for 39%.  28 sequences of 26,033 positions, 4 KV heads,
+// 63 rows: 261 us, 1.5 TB/s.  Measured on the way, with codes not yet centred (then 250 us): every
+// expanding warp with its own cp.async ring instead of a copying warp 269; the positions' factors
+// loaded where they are used 274; 64 columns at a time 293.  Centred: one code for K's and V's
+// expansion 274, the four steps of an expansion unrolled together 275.
 // Every wait on an mbarrier is bounded (see sd_set_wait_timeout_ns); on expiry the CTA records
 // SD_DEVERR_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
 #include <type_traits>

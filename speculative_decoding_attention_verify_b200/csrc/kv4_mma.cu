@@ -618,9 +618,9 @@ cudaError_t launch_d(const Kv4Params &p, cudaStream_t s) {
 }  // namespace
 
 // From 17 rows on the tcgen05 kernel is faster (28 sequences of 26,027 positions, 4 KV heads: this
-// kernel with 32 rows per warp took 228 us for 21 rows and 230 for 28, the tcgen05 one 216 and 219;
-// one sequence of 8,710 and 28 rows 24.1 against 22.7).  Up to 16 this one is: 187 against 210 us
-// for 14 rows, 15.1 against 16.8 for the one sequence.
+// kernel with 32 rows per warp took 228 us for 21 rows and 230 for 28, the tcgen05 one takes 222 and
+// 224; one sequence of 8,710 and 28 rows 24.1 against 18.0).  Up to 16 this one is: 186 against 220 us
+// for 14 rows, 15.6 against 17.8 for the one sequence.
 int kv4_mma_max_rows() { return 16; }
 
 void kv4_mma_plan(int *tile, int *per_sm) {

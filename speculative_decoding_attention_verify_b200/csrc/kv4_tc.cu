@@ -36,7 +36,7 @@
 // Bound by the chain of those steps: with two buffers (TMEM has no room for a third beside O and Q)
 // a tile's S, its softmax and its P V follow one another, about 2,600 cycles a tile for 63 rows and
 // 128 channels, of which the softmax has 2,200; the tensor core is busy for 29% of the kernel's
-// time, issue slots for 38%, shared memory for 39%.  28 sequences of 26,033 positions, 4 KV heads,
+// time, issue slots for 42%, shared memory for 38%.  28 sequences of 26,033 positions, 4 KV heads,
 // 63 rows: 261 us, 1.5 TB/s.  Measured on the way, with codes not yet centred (then 250 us): every
 // expanding warp with its own cp.async ring instead of a copying warp 269; the positions' factors
 // loaded where they are used 274; 64 columns at a time 293.  Centred: one code for K's and V's

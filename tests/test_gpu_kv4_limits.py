@@ -128,3 +128,35 @@ def test_empty_batches_of_rows():
     c.queries = sd.Queries(c.queries.q, i32([0, 0, 0]), 1, 64 - 10)
     out, flag = c.run()
     assert flag == 0 and (out == 9).all()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 8, 9, 16, 17])
+def test_rows_at_the_borders_of_the_kernels(n, d, paged):
+    """8 heads of one group: 8, 16, 24, 32, 40, 64, 72, 128 and 136 rows per KV head."""
+    c = Call([n, 129, 1500], [n, 1, n], 8, 1, d, paged, seed=n, pad_rows=1)
+    out, flag = c.run()
+    assert flag == 0
+    c.check(out)
+
+
+@pytest.mark.parametrize("n", [2, 5])
+def test_constant_rows(n):
+    """Rows of one value (s = 0, codes 0) among others, on both tensor-core kernels: they stand for
+    lo, whatever s they are counted with."""
+    for low in (0.0, 3.0, -1e-20, 1e20):
+        c = Call([300], [n], 7, 1, 128, False, seed=n)
+        for w in range(2):
+            codes, param = (x.clone() for x in c.cache.parts[0][w])
+            if w == 1:
+                codes[:, ::3] = 0
+                param[:, ::3, 0] = 0
+                param[:, ::3, 1] = low
+            c.cache.store(w, 0, R.pack(codes), param)
+            c.cache.parts[0][w] = (codes, param)
+            c.cache.kv[0][w] = R.values(R.pack(codes), param)
+        c.kv = c.cache.cuda()
+        out, flag = c.run()
+        assert flag == 0
+        c.check(out)

@@ -590,7 +590,9 @@ SD_API sd_status sd_kv4_attention_workspace_size(const sd_q_desc *q, const sd_kv
  * codes themselves (exact in fp16) and corrected by each row's s and lo, and V's scale is folded
  * into the softmax weights, which are rounded to fp16 (half a step: 2^-11 of a weight, or 2^-35
  * of its row's largest) where they multiply the codes and nowhere else; everything else is fp32.
- * A row of V whose s lies between 0 and 2^-90 counts with s = 2^-90.  bf16 rows run on tensor
+ * A row of V of one value (s = 0) counts with s = 2^-8 |lo| there, and one whose s is then below
+ * 2^-90 with s = 2^-90; a position whose weight times s is below 2^-136 of its row's largest does
+ * not count at all.  s is neither negative nor NaN (what sd_kv4_append writes).  bf16 rows run on tensor
  * cores (up to 128 rows per KV head, q_data and out 16-byte aligned), the rest, without that
  * rounding and lower bound, on CUDA cores.  The kernel for 17 to 128 rows waits with the bound of
  * sd_set_wait_timeout_ns (SD_DEVERR_TIMEOUT).  workspace: 16-byte aligned, not shared with a call

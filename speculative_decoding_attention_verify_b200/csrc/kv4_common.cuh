@@ -72,6 +72,14 @@ constexpr float kTopLog2 = 10.f, kGrowLog2 = 14.f;
 // than 1e-26.
 constexpr float kMinScale = 8.0779357e-28f;  // 2^-90
 
+// The scale that a row of V counts with.  A row of one value (s = 0) has codes 0, so any serves: one
+// well below the row's value, or the weight of a sink of zeros would set the scale of all others'
+// weights, and -8 and + 8 times it (codes taken as c - 8) would not cancel to 2^-17 of the value.
+__device__ __forceinline__ float value_scale(uint32_t w) {
+    const float s = param_scale(w);
+    return fmaxf(s == 0.f ? fabsf(param_low(w)) * 0.00390625f : s, kMinScale);
+}
+
 // Codes at nibble P (0..3) of both halves of w as a pair of fp16 numbers: c 2^-24 (P even) or
 // 16 c 2^-24 (P odd).  w8 is w >> 8.
 template <int P>

@@ -14,7 +14,9 @@
 // with w_j = p_j s_j taken as one exponential, w_j = 2^(x_j + log2 s_j - m), x_j the score in log2
 // units and m a running maximum of the whole exponent.  w is rounded to fp16 (2^-12 of itself; see
 // kTopLog2 for the smallest ones) and p = w / s is not rounded: it enters the sums of the
-// softmax and of p lo in fp32.  Rows of one value (s = 0, codes 0) count with s = 1 there.
+// softmax and of p lo in fp32.  Rows of one value (s = 0, codes 0) count with s = |lo| / 256 there,
+// and no row with less than 2^-90: a sink of zeros, however large its p, then leaves the others'
+// weights the whole range of fp16.
 //
 // Layout.  Everything is transposed: S^T = K Q^T and O^T = V^T P^T by mma.sync m16n8k16 with 16
 // positions (S) or 16 channels (O) as M and 8 rows as N, because few rows would leave most of an
@@ -343,8 +345,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                     const uint32_t kp = par[gq + 8 * h], vp = par[16 + gq + 8 * h];
                     const float ks = param_scale(kp) * p.scale_log2;
                     const float kl = param_low(kp) * p.scale_log2;
-                    float sc = param_scale(vp);
-                    sc = sc == 0.f ? 1.f : fmaxf(sc, kMinScale);
+                    const float sc = value_scale(vp);
                     is[i][h] = rcp(sc);
                     vl[i][h] = param_low(vp) * is[i][h];
                     const float ls = lg2(sc);

@@ -315,10 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                 float *d = f + (j >> 1) * 4 + (j & 1);
                 d[0] = param_scale(wk) * p.scale_log2;
                 d[2] = param_low(wk) * p.scale_log2;
-                // (a V code stands for c - 8: lo moves by 8 s.  Rows of one value have codes 0; any
-                // s serves, and one well below lo lets -8 and + 8 cancel to 2^-17 of lo)
-                float sc = param_scale(wv);
-                sc = fmaxf(sc == 0.f ? fabsf(param_low(wv)) * 0.00390625f : sc, kMinScale);
+                // (a V code stands for c - 8: lo moves by 8 s)
+                const float sc = value_scale(wv);
                 const float inv = rcp(sc);
                 f[2 * kTile + j] = lg2(sc);
                 d[3 * kTile] = inv;

@@ -20,8 +20,9 @@ def test_a_sink_of_one_value(rows, low, log_scale):
     its value row is constant, so it has no scale of its own.  The others' weights, in fp16, must
     not be measured against its weight: with s = |low| / 256 for it, the largest p s is at most
     max(2^-15, the others' 2^-24 2^-6), and a weight is off by 2^-11 of itself or by 2^-35 of that
-    largest: 2^-35 max(p s) sum max(c, |c - 8|) on top of attention_bound's terms."""
-    h_q, h_kv, d, length = 7, 1, 128, 26000
+    largest: 2^-35 max(p s) sum max(c, |c - 8|) on top of attention_bound's terms.  The length is
+    one that a single CTA takes as a whole, so that the sink meets many others in its warp."""
+    h_q, h_kv, d, length = 7, 1, 128, 1280
     c = Call([length], [rows], h_q, h_kv, d, False, seed=rows)
     g = torch.Generator().manual_seed(rows)
     # keys: ones at position 0, zeros elsewhere (s = 0, lo = the value); queries of one sum

@@ -10,13 +10,17 @@
 // again.  The queries are scaled by a power of two per row (their largest to 2^13; bf16's 8 bits
 // fit fp16's 11, and an element has to be 2^-27 of the row's largest to lose any) and the odd
 // channels, whose codes sit in bits 4-7, by 1/16.  For the values
-//     sum_j p_j v_j = sum_j (p_j s_j) c_j + sum_j p_j lo_j
+//     sum_j p_j v_j = sum_j (p_j s_j) (c_j - 8) + sum_j p_j (lo_j + 8 s_j)
 // with w_j = p_j s_j taken as one exponential, w_j = 2^(x_j + log2 s_j - m), x_j the score in log2
 // units and m a running maximum of the whole exponent.  w is rounded to fp16 (2^-12 of itself; see
 // kTopLog2 for the smallest ones) and p = w / s is not rounded: it enters the sums of the
 // softmax and of p lo in fp32.  Rows of one value (s = 0, codes 0) count with s = |lo| / 256 there,
 // and no row with less than 2^-90: a sink of zeros, however large its p, then leaves the others'
-// weights the whole range of fp16.
+// weights the whole range of fp16.  The products are with c, and 8 times the sum of the step's
+// rounded weights (one more product, with ones) is taken from the accumulators after each step:
+// the tensor core cuts towards zero as it accumulates, and the sum of w c would grow to hundreds
+// of times what is left once lo's part is added (140,000 random positions: odd channels off by
+// 6.7e-4 of themselves without, 1.7e-4 with).  Taking 8 from each code cost twice as much.
 //
 // Layout.  Everything is transposed: S^T = K Q^T and O^T = V^T P^T by mma.sync m16n8k16 with 16
 // positions (S) or 16 channels (O) as M and 8 rows as N, because few rows would leave most of an
@@ -59,6 +63,7 @@ constexpr int kStages = 2;
 
 constexpr int kTile = kWarps * kPos;
 constexpr int kCtasPerSm = 2;  // registers of O^T decide
+constexpr uint32_t kOnes = 0x3c003c00u;  // a pair of fp16 ones
 
 template <int D, int NT>
 struct MmaCfg {
@@ -335,7 +340,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                 nm[nt] = make_float2(m[nt][0] == -INFINITY ? 0.f : -m[nt][0],
                                      m[nt][1] == -INFINITY ? 0.f : -m[nt][1]);
             bool grow = false;
-            float is[2][2], vl[2][2];  // 1 / s and lo / s of the values
+            float is[2][2], vl[2][2];  // 1 / s and lo / s + 8 of the values
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t *par =
@@ -347,7 +352,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                     const float kl = param_low(kp) * p.scale_log2;
                     const float sc = value_scale(vp);
                     is[i][h] = rcp(sc);
-                    vl[i][h] = param_low(vp) * is[i][h];
+                    vl[i][h] = fmaf(param_low(vp), is[i][h], 8.f);
                     const float ls = lg2(sc);
                     const float2 ks2 = make_float2(ks, ks), kl2 = make_float2(kl, kl);
                     const float2 ls2 = make_float2(ls, ls);
@@ -415,11 +420,12 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                         for (int e = 0; e < 4; ++e) o[mt][nt][e] *= f[e & 1];
                 }
             }
+            uint32_t pts[2][NT][2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint8_t *pg = st + i * C::kPageBytes;
                 // ---- weights, and their transpose in operand layout ----
-                uint32_t pt[NT][2];
+                uint32_t (&pt)[NT][2] = pts[i];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -471,6 +477,25 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             mma16816(o[4 * w + 2 * h + 1][nt], b0, b1, b2, b3, pt[nt][0], pt[nt][1]);
+                    }
+            }
+            // ---- 8 times the weights' sums, as rounded, off every channel ----
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float sw[4] = {0.f, 0.f, 0.f, 0.f};  // of columns 2t, 2t + 1, twice
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    mma16816(sw, kOnes, kOnes, kOnes, kOnes, pts[i][nt][0], pts[i][nt][1]);
+                const float2 s2 = make_float2(sw[0], sw[1]);
+#pragma unroll
+                for (int mt = 0; mt < kKs; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // (h = 1: odd channels, codes 16 times as large)
+                        const float by = h ? -0x1p-17f : -0x1p-21f;
+                        const float2 x = __ffma2_rn(s2, make_float2(by, by),
+                                                    make_float2(o[mt][nt][2 * h], o[mt][nt][2 * h + 1]));
+                        o[mt][nt][2 * h] = x.x;
+                        o[mt][nt][2 * h + 1] = x.y;
                     }
             }
         };

@@ -53,3 +53,58 @@ def test_a_sink_of_one_value(rows, low, log_scale):
     bound = bound + 2.0 ** -35 * top * most
     err = (out.double() - ref).abs()
     assert (err <= bound).all(), (err / bound).max()
+
+
+class Long:
+    """One sequence in a contiguous cache on the GPU, and 64-bit attention over it there."""
+
+    def __init__(self, q, h_kv, codes, param):
+        rows, h_q, d = q.shape
+        length = codes[0].shape[1]
+        self.shape, self.q = (length, rows, h_q, h_kv, d), q
+        self.codes, self.param = codes, param
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        kv = sd.KV4Cache(*(R.pack(c)[None].contiguous() for c in codes),
+                         *(x[None].contiguous() for x in param), i32([length]))
+        self.out = sd.sd_kv4_verify_attention(
+            sd.Queries(self.q, i32([0, rows]), rows, length), kv).double()
+
+    def weights(self, head):
+        """Softmax weights [rows][length] of a query head, in 64 bits."""
+        length, rows, h_q, h_kv, d = self.shape
+        g = head // (h_q // h_kv)
+        k = self.param[0][g, :, 1:].double() + self.param[0][g, :, :1].double() * self.codes[0][g].double()
+        s = (self.q[:, head].double() @ k.T) / math.sqrt(d)
+        j = torch.arange(length, device="cuda")
+        hide = j[None] > (length - rows + torch.arange(rows, device="cuda"))[:, None]
+        return torch.softmax(s.masked_fill(hide, -math.inf), -1)
+
+
+@pytest.mark.parametrize("odd", [1])
+@pytest.mark.parametrize("rows", [1, 2, 5, 9])
+def test_values_that_cancel(rows, odd):
+    """140,000 positions in pairs of one key, values s (c - 8) and -s (c - 8) with s = 1 (lo = -8, c
+    from 1 to 15): the exact output of a row that sees whole pairs is zero, and the rounding of a
+    pair's weights cancels too (the same weight multiplies c - 8 and 8 - c).  What is left is how
+    the products are summed.  A sum of 16 products and an accumulator in 24 bits cuts each term at
+    2^-23 of the largest, and a product is at most 8 w: 17 2^-23 8 max(w) for 16 positions.  1 / s,
+    lo / s + 8 and their sums are fp32: 8 2^-23 sum(p) = 2^-20.  An unpaired last position has its
+    weight's rounding, 2^-11 8 p; the output is rounded once."""
+    h_q, h_kv, d, length = 28, 4, 128, 140000
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    rnd = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device="cuda", dtype=torch.uint8)  # noqa: E731
+    kc = rnd(0, 16, h_kv, length // 2, d).repeat_interleave(2, 1)
+    half = rnd(1, 16, h_kv, length // 2, d)
+    vc = torch.stack([half, 16 - half], 2).flatten(1, 2)
+    param = lambda s, lo: torch.tensor([s, lo], device="cuda").to(BF).expand(h_kv, length, 2)  # noqa: E731
+    q = torch.randn(rows, h_q, d, generator=g, device="cuda").to(BF)
+    c = Long(q, h_kv, (kc, vc), (param(0.35, -2.6), param(1.0, -8.0)))
+    for head in range(h_q):
+        p = c.weights(head)
+        ref = p @ (vc[head // 7].double() - 8)
+        tol = 17 * 2.0 ** -23 * 8 * p.view(rows, -1, 16).amax(-1).sum(-1) + 2.0 ** -20
+        seen = length - rows + 1 + torch.arange(rows, device="cuda")
+        last = p[torch.arange(rows, device="cuda"), seen - 1] * (seen % 2)
+        tol = tol + 2.0 ** -11 * 8 * last
+        err = ((c.out[:, head] - ref).abs() - 2.0 ** -8 * ref.abs())[:, odd::2]
+        assert (err <= tol[:, None]).all(), (head, (err / tol[:, None]).max().item())

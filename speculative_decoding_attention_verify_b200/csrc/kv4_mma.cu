@@ -20,7 +20,11 @@
 // rounded weights (one more product, with ones) is taken from the accumulators after each step:
 // the tensor core cuts towards zero as it accumulates, and the sum of w c would grow to hundreds
 // of times what is left once lo's part is added (140,000 random positions: odd channels off by
-// 6.7e-4 of themselves without, 1.7e-4 with).  Taking 8 from each code cost twice as much.
+// 6.7e-4 of themselves without, 1.7e-4 with).  Taking 8 from each code cost twice as much.  All of
+// V's codes are moved to bits 4-7: the tensor core aligns a product by its factors' exponent fields,
+// which for a subnormal say 2^-14, and cuts what lies 24 bits below the largest, so that codes in
+// bits 0-3 lose four bits more than those in bits 4-7 (even channels off by 1.9e-3, now 1.9e-4; the
+// scores' products, of factors that differ less, lose nothing that shows).
 //
 // Layout.  Everything is transposed: S^T = K Q^T and O^T = V^T P^T by mma.sync m16n8k16 with 16
 // positions (S) or 16 channels (O) as M and 8 rows as N, because few rows would leave most of an
@@ -88,6 +92,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Codes at nibble P (0..3) of both halves of w as a pair of fp16 numbers c / kVOne, all four at bits
+// 4-7 of an operand.
+constexpr float kVOne = 1048576.f;  // 2^20
+template <int P>
+__device__ __forceinline__ uint32_t high_codes_at(uint32_t w) {
+    return (P == 0 ? w << 4 : P == 1 ? w : P == 2 ? w >> 4 : w >> 8) & 0x00f000f0u;
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -466,14 +478,13 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t x = __byte_perm(vw[0][w], vw[1][w], h ? 0x7632 : 0x5410);
                         const uint32_t y = __byte_perm(vw[2][w], vw[3][w], h ? 0x7632 : 0x5410);
-                        const uint32_t x8 = x >> 8, y8 = y >> 8;
-                        const uint32_t a0 = codes_at<0>(x, x8), a1 = codes_at<1>(x, x8);
-                        const uint32_t a2 = codes_at<0>(y, y8), a3 = codes_at<1>(y, y8);
+                        const uint32_t a0 = high_codes_at<0>(x), a1 = high_codes_at<1>(x);
+                        const uint32_t a2 = high_codes_at<0>(y), a3 = high_codes_at<1>(y);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             mma16816(o[4 * w + 2 * h][nt], a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
-                        const uint32_t b0 = codes_at<2>(x, x8), b1 = codes_at<3>(x, x8);
-                        const uint32_t b2 = codes_at<2>(y, y8), b3 = codes_at<3>(y, y8);
+                        const uint32_t b0 = high_codes_at<2>(x), b1 = high_codes_at<3>(x);
+                        const uint32_t b2 = high_codes_at<2>(y), b3 = high_codes_at<3>(y);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             mma16816(o[4 * w + 2 * h + 1][nt], b0, b1, b2, b3, pt[nt][0], pt[nt][1]);
@@ -487,13 +498,13 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                 for (int i = 0; i < 2; ++i)
                     mma16816(sw, kOnes, kOnes, kOnes, kOnes, pts[i][nt][0], pts[i][nt][1]);
                 const float2 s2 = make_float2(sw[0], sw[1]);
+                const float2 by = make_float2(-8.f / kVOne, -8.f / kVOne);
 #pragma unroll
                 for (int mt = 0; mt < kKs; ++mt)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {  // (h = 1: odd channels, codes 16 times as large)
-                        const float by = h ? -0x1p-17f : -0x1p-21f;
-                        const float2 x = __ffma2_rn(s2, make_float2(by, by),
-                                                    make_float2(o[mt][nt][2 * h], o[mt][nt][2 * h + 1]));
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 x = __ffma2_rn(
+                            s2, by, make_float2(o[mt][nt][2 * h], o[mt][nt][2 * h + 1]));
                         o[mt][nt][2 * h] = x.x;
                         o[mt][nt][2 * h + 1] = x.y;
                     }
@@ -592,9 +603,8 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
                     float x[D / 8];
 #pragma unroll
                     for (int mt = 0; mt < kKs; ++mt) {
-                        // (codes of odd channels were 16 times as large)
-                        x[2 * mt] = fmaf(o[mt][nt][c], 16777216.f, cr[nt][c]);
-                        x[2 * mt + 1] = fmaf(o[mt][nt][2 + c], 1048576.f, cr[nt][c]);
+                        x[2 * mt] = fmaf(o[mt][nt][c], kVOne, cr[nt][c]);
+                        x[2 * mt + 1] = fmaf(o[mt][nt][2 + c], kVOne, cr[nt][c]);
                     }
                     if (starts && ends) {
                         const float inv = l[nt][c] == 0.f ? 0.f : 1.f / l[nt][c];

@@ -173,13 +173,23 @@ class KVCache:
 
     Contiguous: ``k``, ``v`` of shape [batch][h_kv][l_cap][head_dim].
     Paged: ``k``, ``v`` of shape [num_pages][h_kv][16][head_dim] with ``block_table``
-    [batch][max_pages] int32.  ``kv_len``: int32 [batch] on the GPU.
+    [batch][max_pages] int32.  ``kv_len``: int32 [batch] on the GPU.  The tensors may hold more
+    sequences than ``kv_len`` does, never fewer: appends write where these say.
     """
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, kv_len: torch.Tensor,
                  block_table: Optional[torch.Tensor] = None):
         if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4:
             raise ValueError("KVCache: k and v must be 4-D tensors of one shape and dtype")
+        if kv_len.dtype != torch.int32 or kv_len.dim() != 1:
+            raise ValueError("KVCache: kv_len must be an int32 vector")
+        if block_table is not None and (block_table.dtype != torch.int32 or block_table.dim() != 2):
+            raise ValueError("KVCache: block_table must be an int32 matrix")
+        for t in (v, kv_len, block_table):
+            if t is not None and t.device != k.device:
+                raise ValueError("KVCache: tensors must live on one device")
+        if (k if block_table is None else block_table).shape[0] < kv_len.shape[0]:
+            raise ValueError("KVCache: kv_len holds more sequences than the cache")
         self.k, self.v, self.kv_len, self.block_table = k, v, kv_len, block_table
         d = sd_kv_desc()
         d.dtype = _dtype_code(k)

@@ -229,6 +229,8 @@ class Queries:
 
     def __init__(self, q: torch.Tensor, q_start: torch.Tensor, max_q_rows: int, max_kv_len: int,
                  softmax_scale: float = 0.0):
+        if q_start.dtype != torch.int32 or q_start.dim() != 1 or q_start.device != q.device:
+            raise ValueError("Queries: q_start must be an int32 vector on the queries' device")
         self.q, self.q_start = q, q_start
         d = sd_q_desc()
         d.h_q = q.shape[1]

@@ -1,4 +1,4 @@
-"""Descriptors of caches refuse tensors whose lengths, page tables or types do not fit, before any
+"""Descriptors of caches and queries refuse tensors whose lengths, tables or types do not fit, before any
 pointer is taken (so without a GPU): an append would write where they say."""
 import pytest
 import torch
@@ -45,3 +45,14 @@ def test_what_fits_goes_on_to_the_next_check():
     for kw in (dict(), dict(batch=3), dict(table=torch.zeros(5, 3, dtype=torch.int32))):
         with pytest.raises(ValueError, match="on the GPU"):
             kv(**kw)
+
+
+def test_row_starts_of_queries():
+    """(an int64 vector would be read as twice as many sequences' starts)"""
+    q = torch.zeros(4, 8, 64, dtype=torch.bfloat16)
+    for bad in (torch.zeros(3, dtype=torch.int64), torch.zeros(3, 1, dtype=torch.int32),
+                torch.zeros(3, dtype=torch.int32, device="meta")):
+        with pytest.raises(ValueError, match="q_start must be"):
+            sd.Queries(q, bad, 2, 16)
+    with pytest.raises(ValueError, match="on the GPU"):
+        sd.Queries(q, torch.zeros(3, dtype=torch.int32), 2, 16)

@@ -527,7 +527,8 @@ typedef struct {
  * A sequence with kv_len[b] < n, kv_len[b] > max_kv_len, more positions than max_pages_per_seq
  * pages hold, or rows outside [0, n_rows] sets SD_DEVERR_SHAPE and is skipped; a page index
  * outside the pool sets SD_DEVERR_PAGE and the row's key and value are skipped.  Two sequences
- * must not own the slot of one new row.  n_rows == 0 returns SD_OK and launches nothing.
+ * must not own the slot of one new row.  n_rows == 0 returns SD_OK and launches nothing (q, k, v
+ * and q_out may then be NULL).
  */
 SD_API sd_status sd_kv_append(const sd_rope_desc *rope, const sd_rows_desc *rows,
                               const sd_kv_desc *cache, int32_t batch, void *q_out,

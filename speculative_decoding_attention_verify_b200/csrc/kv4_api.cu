@@ -90,10 +90,12 @@ sd_status make_rope(const sd_rope_desc *r, int head_dim, RopeParams *out) {
 // Checks of the rows of an append and their share of its parameters; *wide: 16-byte accesses fit.
 sd_status fill_rows(const sd_rope_desc *rope, const sd_rows_desc *rows, int dtype, int h_kv,
                     int head_dim, int batch, void *q_out, AppendParams *p, bool *wide) {
-    if (!rows || !rows->q_start || !rows->k || !rows->v || rows->h_q < 0 || rows->n_rows < 0 ||
+    if (!rows || !rows->q_start || rows->h_q < 0 || rows->n_rows < 0 ||
         rows->n_rows > (1 << 30) || rows->max_kv_len < 1)
         return SD_ERR_INVALID_ARG;
-    if ((rows->h_q > 0) != (rows->q != nullptr) || (rows->h_q > 0) != (q_out != nullptr))
+    // (an empty tensor may have no address)
+    if (rows->n_rows > 0 && (!rows->k || !rows->v || (rows->h_q > 0) != (rows->q != nullptr) ||
+                             (rows->h_q > 0) != (q_out != nullptr)))
         return SD_ERR_INVALID_ARG;
     if (rows->h_q > 65535) return SD_ERR_INVALID_ARG;
     const int64_t kw = (int64_t)h_kv * head_dim, qw = (int64_t)rows->h_q * head_dim;

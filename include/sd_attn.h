@@ -498,7 +498,8 @@ typedef struct {
  * elements, at least heads * head_dim, so the three may be parts of one projection's output).
  * Sequence b owns rows [q_start[b], q_start[b+1]) (device int32 [batch+1]); they are the LAST
  * n of its cache's kv_len[b] positions, as in the attention calls: row i goes to position
- * kv_len[b] - n + i.  Rows from q_start[batch] on (padding) are neither read nor written.
+ * kv_len[b] - n + i.  Rows from q_start[batch] on (padding) have no effect, whatever they hold, and
+ * their rows of the outputs are left as they were.
  *
  *  h_q         query heads (0 with q NULL: keys and values alone).
  *  n_rows      host: rows that q, k and v hold; every q_start entry is at most n_rows.
@@ -525,7 +526,8 @@ typedef struct {
  * than their type's; 16-byte aligned pointers and strides take wide copies.
  *
  * A sequence with kv_len[b] < n, kv_len[b] > max_kv_len, more positions than max_pages_per_seq
- * pages hold, or rows outside [0, n_rows] sets SD_DEVERR_SHAPE and is skipped; a page index
+ * pages hold, or rows outside [0, n_rows] sets SD_DEVERR_SHAPE and is skipped (so does a q_start
+ * that decreases, where rows of other sequences may be skipped too); a page index
  * outside the pool sets SD_DEVERR_PAGE and the row's key and value are skipped.  Two sequences
  * must not own the slot of one new row.  n_rows == 0 returns SD_OK and launches nothing (q, k, v
  * and q_out may then be NULL).

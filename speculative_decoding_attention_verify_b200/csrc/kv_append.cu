@@ -159,6 +159,16 @@ __device__ __forceinline__ RowInfo find_row(const AppendParams &p, int r, int la
     return f;
 }
 
+// Block 0 reports the row starts that no row of the launch meets: negative or decreasing ones, and
+// rows that begin at or behind n_rows.  (The blocks read q_start for their rows anyway.)
+__device__ __forceinline__ void check_starts(const AppendParams &p) {
+    if (blockIdx.x != 0) return;
+    for (int b = threadIdx.x; b < p.batch; b += kThreads) {
+        const int q0 = __ldg(p.q_start + b), q1 = __ldg(p.q_start + b + 1);
+        if (q0 < 0 || q1 < q0 || q1 > p.n_rows) set_dev_err(p.dev_err, SD_DEVERR_SHAPE);
+    }
+}
+
 // Position of row r, in turns of pair m, reduced to [-1/2, 1/2].
 __device__ __forceinline__ double turn_of(const AppendParams &p, const RowInfo &f, int r, int m) {
     const int pos = p.pos ? __ldg(p.pos + r) : f.j;
@@ -249,6 +259,7 @@ append_kernel(const __grid_constant__ AppendParams p) {
                 s_cs[row][m % VEC][m / VEC] = cos_sin(p, t);
             }
         }
+    check_starts(p);
     __syncthreads();
     if (!(f.flags & 1)) return;
     float2 cs[VEC];
@@ -392,6 +403,7 @@ __global__ void __launch_bounds__(kThreads) append_narrow_kernel(const __grid_co
     __shared__ float s_val[KV4 ? kThreads / 32 : 1][KV4 ? D : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x;
     const RowInfo f = find_row(p, r, lane);
+    check_starts(p);
     if (!(f.flags & 1)) return;
     const int rot = p.rope.rotary_dim, half_rot = rot >> 1;
     const bool half = p.rope.layout == SD_ROPE_HALF;

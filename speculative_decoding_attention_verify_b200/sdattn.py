@@ -155,6 +155,17 @@ def _on(t: torch.Tensor):
     return _HERE
 
 
+def _for(stream):
+    """Context in which new tensors belong to the stream that a call runs on.  (Allocated for another
+    one, a workspace could be handed out again, and an output's memory still be in use, while the
+    call runs.)"""
+    if stream is None:
+        return _HERE
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
 def _check(status: int, where: str):
     if status != SD_OK:
         raise SdError(status, where)
@@ -245,12 +256,13 @@ class Queries:
         return self.q.shape[0]
 
 
-def _workspace(nbytes, device, given: Optional[torch.Tensor]):
+def _workspace(nbytes, device, given: Optional[torch.Tensor], stream=None):
     """The caller's workspace (the library checks its size), or a new one of nbytes() bytes (the
     size query only runs when a workspace has to be allocated)."""
     if given is not None:
         return given
-    return torch.empty(max(int(nbytes()), 16), dtype=torch.uint8, device=device)
+    with _for(stream):
+        return torch.empty(max(int(nbytes()), 16), dtype=torch.uint8, device=device)
 
 
 def sd_set_wait_timeout_ns(ns: int) -> int:
@@ -277,14 +289,18 @@ def sd_attention_plan(kind: int, q: Queries, kv: KVCache, extent: int = 0,
     return e.value, n.value
 
 
-def _attn_out(q: Queries, out):
-    return torch.empty_like(q.q) if out is None else out
+def _attn_out(q: Queries, out, stream):
+    if out is not None:
+        return out
+    with _for(stream):
+        return torch.empty_like(q.q)
 
 
 def sd_verify_attention(q: Queries, kv: KVCache, out=None, workspace=None, dev_err=None,
                         stream=None) -> torch.Tensor:
-    out = _attn_out(q, out)
-    ws = _workspace(lambda: sd_attention_workspace_size(SD_ATTN_VERIFY, q, kv), q.q.device, workspace)
+    out = _attn_out(q, out, stream)
+    ws = _workspace(lambda: sd_attention_workspace_size(SD_ATTN_VERIFY, q, kv), q.q.device, workspace,
+                    stream)
     with _on(q.q):
         _check(lib().sd_verify_attention(ctypes.byref(q.desc), _ptr(q.q), ctypes.byref(kv.desc),
                                          kv.batch, _ptr(out), _ptr(ws), ws.numel(), _ptr(dev_err),
@@ -308,8 +324,9 @@ def sd_verify_attention_noalloc(q: Queries, kv: KVCache, out: torch.Tensor, dev_
 def sd_text_anchored_attention(q: Queries, kv: KVCache, vis_begin, vis_end, window,
                                max_window: int, out=None, workspace=None, dev_err=None,
                                stream=None) -> torch.Tensor:
-    out = _attn_out(q, out)
-    ws = _workspace(lambda: sd_attention_workspace_size(SD_ATTN_TEXT_ANCHORED, q, kv), q.q.device, workspace)
+    out = _attn_out(q, out, stream)
+    ws = _workspace(lambda: sd_attention_workspace_size(SD_ATTN_TEXT_ANCHORED, q, kv), q.q.device,
+                    workspace, stream)
     with _on(q.q):
         _check(lib().sd_text_anchored_attention(
             ctypes.byref(q.desc), _ptr(q.q), ctypes.byref(kv.desc), kv.batch, _ptr(vis_begin),
@@ -320,9 +337,9 @@ def sd_text_anchored_attention(q: Queries, kv: KVCache, vis_begin, vis_end, wind
 
 def sd_sparse_attention(q: Queries, kv: KVCache, idx: torch.Tensor, tail_begin, max_tail: int,
                         out=None, workspace=None, dev_err=None, stream=None) -> torch.Tensor:
-    out = _attn_out(q, out)
+    out = _attn_out(q, out, stream)
     ws = _workspace(lambda: sd_sparse_workspace_size(q, kv, int(idx.shape[-1]), max_tail), q.q.device,
-                    workspace)
+                    workspace, stream)
     with _on(q.q):
         _check(lib().sd_sparse_attention(
             ctypes.byref(q.desc), _ptr(q.q), ctypes.byref(kv.desc), kv.batch, _ptr(idx),
@@ -351,8 +368,9 @@ def sd_sparse_stage(kv: KVCache, idx: torch.Tensor, tail_begin, selection=None, 
     """Stages the selected rows of idx [batch][h_kv][k]; returns the selection buffer."""
     k = int(idx.shape[-1])
     if selection is None:
-        selection = torch.empty(max(sd_sparse_selection_size(kv, k), 16), dtype=torch.uint8,
-                                device=kv.k.device)
+        with _for(stream):
+            selection = torch.empty(max(sd_sparse_selection_size(kv, k), 16), dtype=torch.uint8,
+                                    device=kv.k.device)
     with _on(kv.k):
         _check(lib().sd_sparse_stage(ctypes.byref(kv.desc), kv.batch, _ptr(idx), k,
                                      _ptr(tail_begin), _ptr(selection), selection.numel(),
@@ -363,8 +381,8 @@ def sd_sparse_stage(kv: KVCache, idx: torch.Tensor, tail_begin, selection=None, 
 def sd_sparse_attention_staged(q: Queries, kv: KVCache, selection: torch.Tensor, k: int,
                                tail_begin, max_tail: int, out=None, workspace=None, dev_err=None,
                                stream=None) -> torch.Tensor:
-    out = _attn_out(q, out)
-    ws = _workspace(lambda: sd_sparse_workspace_size(q, kv, k, max_tail), q.q.device, workspace)
+    out = _attn_out(q, out, stream)
+    ws = _workspace(lambda: sd_sparse_workspace_size(q, kv, k, max_tail), q.q.device, workspace, stream)
     with _on(q.q):
         _check(lib().sd_sparse_attention_staged(
             ctypes.byref(q.desc), _ptr(q.q), ctypes.byref(kv.desc), kv.batch, _ptr(selection),
@@ -383,8 +401,9 @@ def sd_topk_workspace_size(kv: KVCache, max_cand: int, k: int) -> int:
 def sd_topk_select(q: Queries, kv: KVCache, cand_begin, cand_end, max_cand: int, k: int,
                    idx_out=None, workspace=None, dev_err=None, stream=None) -> torch.Tensor:
     if idx_out is None:
-        idx_out = torch.empty((kv.batch, kv.h_kv, int(k)), dtype=torch.int32, device=q.q.device)
-    ws = _workspace(lambda: sd_topk_workspace_size(kv, max_cand, k), q.q.device, workspace)
+        with _for(stream):
+            idx_out = torch.empty((kv.batch, kv.h_kv, int(k)), dtype=torch.int32, device=q.q.device)
+    ws = _workspace(lambda: sd_topk_workspace_size(kv, max_cand, k), q.q.device, workspace, stream)
     with _on(q.q):
         _check(lib().sd_topk_select(
             ctypes.byref(q.desc), _ptr(q.q), ctypes.byref(kv.desc), kv.batch, _ptr(cand_begin),
@@ -410,9 +429,10 @@ def sd_topk_select_scored(mode: int, q: Queries, kv: KVCache, cand_begin, cand_e
     SD_TOPK_MEAN_TEXT_ATTENTION (q holds the prefill text rows).  scores_out: optional float64
     [batch][h_kv][max_cand] tensor that receives every candidate's score."""
     if idx_out is None:
-        idx_out = torch.empty((kv.batch, kv.h_kv, int(k)), dtype=torch.int32, device=q.q.device)
+        with _for(stream):
+            idx_out = torch.empty((kv.batch, kv.h_kv, int(k)), dtype=torch.int32, device=q.q.device)
     ws = _workspace(lambda: sd_topk_scored_workspace_size(mode, q, kv, max_cand, k), q.q.device,
-                    workspace)
+                    workspace, stream)
     with _on(q.q):
         _check(lib().sd_topk_select_scored(
             int(mode), ctypes.byref(q.desc), _ptr(q.q), ctypes.byref(kv.desc), kv.batch,
@@ -465,9 +485,10 @@ def sd_draft_layer(layer: DraftLayer, emb: torch.Tensor, hid: torch.Tensor, cach
     `cache` (whose kv_len already counts them)."""
     n = emb.shape[0]
     if out is None:
-        out = torch.empty((n, layer.d_model), dtype=torch.bfloat16, device=emb.device)
+        with _for(stream):
+            out = torch.empty((n, layer.d_model), dtype=torch.bfloat16, device=emb.device)
     ws = _workspace(lambda: sd_draft_layer_workspace_size(layer, n, cache, max_kv_len, window),
-                    emb.device, workspace)
+                    emb.device, workspace, stream)
     with _on(emb):
         _check(lib().sd_draft_layer(ctypes.byref(layer.desc), _ptr(emb), _ptr(hid), int(n),
                                     ctypes.byref(cache.desc), int(max_kv_len), int(window),
@@ -480,7 +501,8 @@ def sd_hsr_project(emb: torch.Tensor, hid: torch.Tensor, weight: torch.Tensor, b
                    out=None, stream=None) -> torch.Tensor:
     n, dm = emb.shape
     if out is None:
-        out = torch.empty((n, dm), dtype=torch.bfloat16, device=emb.device)
+        with _for(stream):
+            out = torch.empty((n, dm), dtype=torch.bfloat16, device=emb.device)
     with _on(emb):
         _check(lib().sd_hsr_project(_ptr(emb), _ptr(hid), n, dm, _ptr(weight), _ptr(bias),
                                     _ptr(out), _stream(stream)), "sd_hsr_project")
@@ -494,14 +516,22 @@ def sd_accept_workspace_size(batch: int, max_gamma: int, vocab: int) -> int:
     return n.value
 
 
+def _accept_out(n_acc, out_tok, batch: int, max_gamma: int, dev, stream):
+    """The caller's outputs, or new ones (tokens -1 behind the emitted ones)."""
+    with _for(stream if n_acc is None or out_tok is None else None):
+        if n_acc is None:
+            n_acc = torch.empty(batch, dtype=torch.int32, device=dev)
+        if out_tok is None:
+            out_tok = torch.full((batch, max_gamma + 1), -1, dtype=torch.int32, device=dev)
+    return n_acc, out_tok
+
+
 def sd_accept_greedy(tgt_logits, draft_tok, gamma, max_gamma: int, n_acc=None, out_tok=None,
                      workspace=None, dev_err=None, stream=None):
     batch, vocab = gamma.shape[0], tgt_logits.shape[1]
     dev = tgt_logits.device
-    n_acc = torch.empty(batch, dtype=torch.int32, device=dev) if n_acc is None else n_acc
-    if out_tok is None:
-        out_tok = torch.full((batch, max_gamma + 1), -1, dtype=torch.int32, device=dev)
-    ws = _workspace(lambda: sd_accept_workspace_size(batch, max_gamma, vocab), dev, workspace)
+    n_acc, out_tok = _accept_out(n_acc, out_tok, batch, max_gamma, dev, stream)
+    ws = _workspace(lambda: sd_accept_workspace_size(batch, max_gamma, vocab), dev, workspace, stream)
     with _on(tgt_logits):
         _check(lib().sd_accept_greedy(_ptr(tgt_logits), _ptr(draft_tok), _ptr(gamma), batch,
                                       int(max_gamma), vocab, _ptr(n_acc), _ptr(out_tok),
@@ -515,12 +545,11 @@ def sd_accept_sample(tgt_logits, draft_logits, draft_tok, u, v, gamma, max_gamma
                      stream=None):
     batch, vocab = gamma.shape[0], tgt_logits.shape[1]
     dev = tgt_logits.device
-    n_acc = torch.empty(batch, dtype=torch.int32, device=dev) if n_acc is None else n_acc
-    if out_tok is None:
-        out_tok = torch.full((batch, max_gamma + 1), -1, dtype=torch.int32, device=dev)
+    n_acc, out_tok = _accept_out(n_acc, out_tok, batch, max_gamma, dev, stream)
     if near_boundary is None:
-        near_boundary = torch.zeros(batch, dtype=torch.int32, device=dev)
-    ws = _workspace(lambda: sd_accept_workspace_size(batch, max_gamma, vocab), dev, workspace)
+        with _for(stream):
+            near_boundary = torch.zeros(batch, dtype=torch.int32, device=dev)
+    ws = _workspace(lambda: sd_accept_workspace_size(batch, max_gamma, vocab), dev, workspace, stream)
     with _on(tgt_logits):
         _check(lib().sd_accept_sample(_ptr(tgt_logits), _ptr(draft_logits), _ptr(draft_tok),
                                       _ptr(u), _ptr(v), _ptr(gamma), batch, int(max_gamma), vocab,
@@ -701,14 +730,15 @@ def _check_rows(rows: NewRows, cache, where: str):
         raise ValueError(f"{where}: max_kv_len exceeds the cache's room")
 
 
-def _rows_out(out, like: Optional[torch.Tensor], where: str):
+def _rows_out(out, like: Optional[torch.Tensor], where: str, stream=None):
     """The caller's output for rows shaped as `like`, or a new one."""
     if like is None:
         if out is not None:
             raise ValueError(f"{where}: q_out without q")
         return None
     if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        with _for(stream):
+            return torch.empty(like.shape, dtype=like.dtype, device=like.device)
     if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device:
         raise ValueError(f"{where}: an output must have the shape, dtype and device of its rows")
     return out
@@ -719,7 +749,7 @@ def sd_kv_append(rope: Optional[Rope], rows: NewRows, cache: KVCache, q_out=None
     """Rotates the rows' queries and keys and writes keys and values into the cache, whose kv_len
     already counts them.  Returns the rotated queries (None without queries)."""
     _check_rows(rows, cache, "sd_kv_append")
-    q_out = _rows_out(q_out, rows.q, "sd_kv_append")
+    q_out = _rows_out(q_out, rows.q, "sd_kv_append", stream)
     with _on(rows.k):
         _check(lib().sd_kv_append(rope.ref if rope is not None else None, rows.ref, cache.ref,
                                   rows.batch, _ptr(q_out), _ptr(dev_err), _stream(stream)),
@@ -732,7 +762,7 @@ def sd_kv4_append(rope: Optional[Rope], rows: NewRows, cache: KV4Cache, q_out=No
     """sd_kv_append into a 4-bit cache.  k_out, v_out: optional tensors like the rows' k and v that
     receive the values the stored rows stand for."""
     _check_rows(rows, cache, "sd_kv4_append")
-    q_out = _rows_out(q_out, rows.q, "sd_kv4_append")
+    q_out = _rows_out(q_out, rows.q, "sd_kv4_append", stream)
     for t in (k_out, v_out):
         if t is not None:
             _rows_out(t, rows.k, "sd_kv4_append")
@@ -761,8 +791,8 @@ def sd_kv4_verify_attention(q: Queries, kv: KV4Cache, out=None, workspace=None, 
                          "batch or device")
     if kv.room is not None and q.desc.max_kv_len > kv.room:
         raise ValueError("sd_kv4_verify_attention: max_kv_len exceeds the cache's room")
-    out = _rows_out(out, t, "sd_kv4_verify_attention")
-    ws = _workspace(lambda: sd_kv4_attention_workspace_size(q, kv), t.device, workspace)
+    out = _rows_out(out, t, "sd_kv4_verify_attention", stream)
+    ws = _workspace(lambda: sd_kv4_attention_workspace_size(q, kv), t.device, workspace, stream)
     with _on(t):
         _check(lib().sd_kv4_verify_attention(q.ref, _ptr(t), kv.ref, kv.row_shape[3], _ptr(out),
                                              _ptr(ws), ws.numel(), _ptr(dev_err), _stream(stream)),

@@ -599,7 +599,7 @@ SD_API sd_status sd_kv4_attention_workspace_size(const sd_q_desc *q, const sd_kv
  * cores (up to 128 rows per KV head, q_data and out 16-byte aligned), the rest, without that
  * rounding and lower bound, on CUDA cores.  The kernel for 17 to 128 rows waits with the bound of
  * sd_set_wait_timeout_ns (SD_DEVERR_TIMEOUT).  workspace: 16-byte aligned, not shared with a call
- * in flight.  A sequence whose hints are violated (more than max_q_rows rows, kv_len
+ * in flight.  max_kv_len is 2^30 at most (SD_ERR_INVALID_ARG).  A sequence whose hints are violated (more than max_q_rows rows, kv_len
  * below its rows or above max_kv_len or its pages) sets SD_DEVERR_SHAPE and its rows of out are
  * left as they were; rows on a page outside the pool (SD_DEVERR_PAGE) count as zeros.
  */

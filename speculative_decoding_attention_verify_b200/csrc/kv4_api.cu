@@ -148,8 +148,8 @@ sd_status plan_kv4(const sd_q_desc *q, const sd_kv4_desc *kv, int batch, Kv4Plan
         return SD_ERR_INVALID_ARG;
     if (st != SD_OK) return st;
     const long long rows = (long long)(q->h_q / kv->h_kv) * q->max_q_rows;
-    // (rows of all units, and the grids of the merge)
-    if ((long long)batch * q->max_q_rows > (1LL << 30) || rows > 65535 ||
+    // (rows of all units, the grids of the merge, and positions rounded up to a tile's end)
+    if (q->max_kv_len > (1 << 30) || (long long)batch * q->max_q_rows > (1LL << 30) || rows > 65535 ||
         (long long)batch * kv->h_kv > (1LL << 30))
         return SD_ERR_INVALID_ARG;
     *plan = Kv4Plan{};

@@ -79,9 +79,9 @@ def test_tokens_of_acceptance():
     gamma = torch.tensor([2, 2], dtype=torch.int32, device="cuda")
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    busy = torch.empty(1 << 26, device="cuda")
-    for _ in range(20):
-        busy.fill_(1.0)  # (keeps the current stream behind)
+    busy = torch.empty(1 << 28, device="cuda")
+    for _ in range(300):
+        busy.fill_(1.0)  # (keeps the current stream behind for some tens of milliseconds)
     n, tok = sd.sd_accept_greedy(logits, draft, gamma, 2, stream=side)
     side.synchronize()
     got = torch.empty_like(tok)

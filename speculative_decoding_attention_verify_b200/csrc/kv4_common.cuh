@@ -62,11 +62,12 @@ __device__ __forceinline__ void cp_async4z(uint32_t dst, const void *src, int n)
                  : "memory");
 }
 
-// Exponents of the weights.  A maximum is set so that the largest weight becomes 2^kTopLog2, and
-// moves only when one would exceed 2^kGrowLog2 (fp16 ends at 2^16).  fp16's smallest step is 2^-24,
-// so a weight is off by 2^-12 of itself or by 2^-35 of its row's largest, whichever is more: 140,000
+// Exponents of the weights.  A maximum is set so that the largest weight becomes 2^kTopLog2 (or up to
+// twice that, in whole steps), and moves only when one would exceed 2^kGrowLog2 (fp16 ends below
+// 2^16).  fp16's smallest step is 2^-24,
+// so a weight is off by 2^-11 of itself or by 2^-35 of its row's largest, whichever is more: 140,000
 // positions of next to no weight lose 2^-18 together, where a largest weight of 1 would lose 2^-8.
-constexpr float kTopLog2 = 10.f, kGrowLog2 = 14.f;
+constexpr float kTopLog2 = 10.f, kGrowLog2 = 15.f;
 
 // A scale below this is taken for it: 1 / s stays in range, and codes of such rows are worth less
 // than 1e-26.

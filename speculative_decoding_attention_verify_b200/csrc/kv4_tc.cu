@@ -651,7 +651,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
                             float x = fmaxf(mx[k], __shfl_xor_sync(FULL, mx[k], 1));
                             x = fmaxf(x, __shfl_xor_sync(FULL, x, 2));
                             const bool up = x > (mk[k] == -INFINITY ? -INFINITY : kGrowLog2);
-                            x -= kTopLog2;
+                            // (whole steps: the tile's earlier weights, rounded already, take a
+                            // power of two exactly)
+                            x = floorf(x - kTopLog2);
                             f[k] = up && mk[k] != -INFINITY ? ex2(-x) : 1.f;
                             if (up) {
                                 mk[k] = x - nm[k];

@@ -58,7 +58,7 @@ def test_a_sink_of_one_value(rows, low, log_scale):
 class Long:
     """One sequence in a contiguous cache on the GPU, and 64-bit attention over it there."""
 
-    def __init__(self, q, h_kv, codes, param):
+    def __init__(self, q, h_kv, codes, param, softmax_scale=0.0):
         rows, h_q, d = q.shape
         length = codes[0].shape[1]
         self.shape, self.q = (length, rows, h_q, h_kv, d), q
@@ -67,7 +67,7 @@ class Long:
         kv = sd.KV4Cache(*(R.pack(c)[None].contiguous() for c in codes),
                          *(x[None].contiguous() for x in param), i32([length]))
         self.out = sd.sd_kv4_verify_attention(
-            sd.Queries(self.q, i32([0, rows]), rows, length), kv).double()
+            sd.Queries(self.q, i32([0, rows]), rows, length, softmax_scale), kv).double()
 
     def weights(self, head):
         """Softmax weights [rows][length] of a query head, in 64 bits."""
@@ -139,3 +139,30 @@ def test_long_random_contexts(rows):
             total[i] += x.view(-1, 2).sum(0)
     ratio = (total[0] / (total[1] + total[2])).sqrt()
     assert (ratio <= 1.02).all(), ratio.tolist()
+
+
+@pytest.mark.parametrize("A,B", [(0.9921875, 4.96875), (0.671875, 4.3125)])
+@pytest.mark.parametrize("rows", [1, 2, 3, 9, 10, 18])
+def test_weights_are_rounded_once(rows, A, B):
+    """A row's maximum moves within a tile, after weights of the tile have been rounded: position 0
+    scores 0, positions 1 to 31 A below it, position 40 B above it (in log2 units), the rest nothing.
+    Values are zero: codes 8 with lo = -8, but codes 0 with lo = 0 at positions 1 to 31, so that the
+    output is 8 times the error of their weights, which is half a step, 2^-11, at most; A and B are such
+    that rounding 2^-A and then 2^-B times that gives 1.7 times as much.  Sums in fp32: 2^-20."""
+    h_q, h_kv, d, length = 7, 1, 128, 200
+    score = torch.full((length,), -100.0)
+    score[0], score[1:32], score[40] = 0.0, -A, B
+    assert torch.equal(score, score.to(BF).float())
+    kc = torch.zeros(h_kv, length, d, dtype=torch.uint8, device="cuda")
+    kp = torch.stack([torch.zeros(length), score], -1).to(BF)[None].cuda()
+    low = torch.zeros(length, dtype=torch.bool)
+    low[1:32] = True
+    vc = torch.where(low, 0, 8).to(torch.uint8)[None, :, None].expand(h_kv, length, d).cuda()
+    vp = torch.stack([torch.ones(length), torch.where(low, 0.0, -8.0)], -1).to(BF)[None].cuda()
+    q = torch.zeros(rows, h_q, d, dtype=BF, device="cuda")
+    q[..., 5] = 1.0
+    c = Long(q, h_kv, (kc, vc), (kp, vp), softmax_scale=math.log(2))
+    p = 2.0 ** score.double()
+    share = p[1:32].sum() / p.sum()
+    assert (c.out.abs() <= 2.0 ** -11 * 8 * share * (1 + 2.0 ** -8) + 2.0 ** -20).all(), \
+        (c.out.abs().max() / share * 2 ** 8).item()

@@ -505,7 +505,7 @@ typedef struct {
  *  n_rows      host: rows that q, k and v hold; every q_start entry is at most n_rows.
  *  max_kv_len  host hint >= every kv_len[b]: positions a contiguous cache has room for.
  *  pos         device int32 [n_rows], or NULL: the rows' rotation positions (NULL: their
- *              cache positions).
+ *              cache positions).  One position per row, for all its pairs.
  */
 typedef struct {
     int32_t h_q;
@@ -591,17 +591,21 @@ SD_API sd_status sd_kv4_attention_workspace_size(const sd_q_desc *q, const sd_kv
  * the cache's rows stand for as K and V.  One row per sequence is plain decoding.  q_data and
  * out hold kv->dtype.  Neither K nor V is ever dequantised in memory: scores are formed on the
  * codes themselves (exact in fp16) and corrected by each row's s and lo, and V's scale is folded
- * into the softmax weights, which are rounded to fp16 (half a step: 2^-11 of a weight, or 2^-35
- * of its row's largest) where they multiply the codes and nowhere else; everything else is fp32.
+ * into the softmax weights, which are rounded to fp16 once (half a step: 2^-11 of a weight, or
+ * 2^-35 of its row's largest) where they multiply the codes, taken as c - 8.  Sums are held in fp32;
+ * those of products, in the tensor cores' accumulators, which cut towards zero what lies 24 bits
+ * below a step's largest term.  Over 140,000 random positions all this is off by 2e-4 of the output
+ * (rms), beside its own rounding.
  * A row of V of one value (s = 0) counts with s = 2^-8 |lo| there, and one whose s is then below
  * 2^-90 with s = 2^-90; a position whose weight times s is below 2^-136 of its row's largest does
- * not count at all.  s is neither negative nor NaN (what sd_kv4_append writes).  bf16 rows run on tensor
- * cores (up to 128 rows per KV head, q_data and out 16-byte aligned), the rest, without that
- * rounding and lower bound, on CUDA cores.  The kernel for 17 to 128 rows waits with the bound of
- * sd_set_wait_timeout_ns (SD_DEVERR_TIMEOUT).  workspace: 16-byte aligned, not shared with a call
- * in flight.  max_kv_len is 2^30 at most (SD_ERR_INVALID_ARG).  A sequence whose hints are violated (more than max_q_rows rows, kv_len
- * below its rows or above max_kv_len or its pages) sets SD_DEVERR_SHAPE and its rows of out are
- * left as they were; rows on a page outside the pool (SD_DEVERR_PAGE) count as zeros.
+ * not count at all.  s is neither negative nor NaN (what sd_kv4_append writes).
+ * bf16 rows run on tensor cores (up to 128 rows per KV head, q_data and out 16-byte aligned), the
+ * rest, without that rounding and those bounds, on CUDA cores, many times slower.  The kernel for 17
+ * to 128 rows waits with the bound of sd_set_wait_timeout_ns (SD_DEVERR_TIMEOUT).  workspace: 16-byte
+ * aligned, not shared with a call in flight.  max_kv_len is 2^30 at most (SD_ERR_INVALID_ARG).
+ * A sequence whose hints are violated (more than max_q_rows rows, kv_len below its rows or above
+ * max_kv_len or its pages) sets SD_DEVERR_SHAPE and its rows of out are left as they were; rows on a
+ * page outside the pool (SD_DEVERR_PAGE) count as zeros.
  */
 SD_API sd_status sd_kv4_verify_attention(const sd_q_desc *q, const void *q_data,
                                          const sd_kv4_desc *kv, int32_t batch, void *out,

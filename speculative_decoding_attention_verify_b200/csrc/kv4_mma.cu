@@ -12,7 +12,7 @@
 // channels, whose codes sit in bits 4-7, by 1/16.  For the values
 //     sum_j p_j v_j = sum_j (p_j s_j) (c_j - 8) + sum_j p_j (lo_j + 8 s_j)
 // with w_j = p_j s_j taken as one exponential, w_j = 2^(x_j + log2 s_j - m), x_j the score in log2
-// units and m a running maximum of the whole exponent.  w is rounded to fp16 (2^-12 of itself; see
+// units and m a running maximum of the whole exponent.  w is rounded to fp16 (2^-11 of itself; see
 // kTopLog2 for the smallest ones) and p = w / s is not rounded: it enters the sums of the
 // softmax and of p lo in fp32.  Rows of one value (s = 0, codes 0) count with s = |lo| / 256 there,
 // and no row with less than 2^-90: a sink of zeros, however large its p, then leaves the others'
@@ -45,9 +45,11 @@
 // positions.
 // Query fragments are registers for up to 8 rows; for more they are read from shared memory, once
 // for both pages.
-// Measured: 28 sequences of 26,025 positions, 4 KV heads, 7 rows: 91-95 us, 4.3 TB/s; one sequence
-// of 140,001 30 us.  Bound by issue slots, about 325 instructions per page of a warp; with bf16
-// operands, whose codes need more instructions per pair, 107 us.
+// Measured: 28 sequences of 26,025 positions, 4 KV heads, 7 rows: 101 us, 3.9 TB/s (in pages 107); one
+// sequence of 140,001 31.5 us.  With 16 warps per SM the ALU pipe is busy for 55% and issue slots
+// for 57% (half the sequences: 315 instructions per page of a warp); warps wait for the pipe and for
+// results in turn.  14 rows take 197 us: at 128 registers that kernel spills 524 bytes, and half of
+// what its warps wait for is local memory (issue slots 40%).
 #include <type_traits>
 
 #include "kv4_common.cuh"
@@ -654,8 +656,8 @@ cudaError_t launch_d(const Kv4Params &p, cudaStream_t s) {
 }  // namespace
 
 // From 17 rows on the tcgen05 kernel is faster (28 sequences of 26,027 positions, 4 KV heads: this
-// kernel with 32 rows per warp took 228 us for 21 rows and 230 for 28, the tcgen05 one takes 222 and
-// 224; one sequence of 8,710 and 28 rows 24.1 against 18.0).  Up to 16 this one is: 186 against 220 us
+// kernel with 32 rows per warp took 228 us for 21 rows and 230 for 28, the tcgen05 one takes 227 and
+// 224; one sequence of 8,710 and 28 rows 24.1 against 18.0).  Up to 16 this one is: 197 against 220 us
 // for 14 rows, 15.6 against 17.8 for the one sequence.
 int kv4_mma_max_rows() { return 16; }
 

@@ -7,6 +7,8 @@
 // each, and a thread owns one channel of the output.  Everything is fp32.  Bound by its shared
 // memory reads (a K and a V value each serve 4 or 8 rows); the splits are joined by
 // kv4_merge_kernel.
+// Far slower than the tensor-core kernels: 4 sequences of 10,000 positions, 4 KV heads, fp32: 7 rows
+// 110 us, 63 rows 814; 2 sequences of 26,043 positions and 133 bf16 rows 2.0 ms.
 #include "kv4_common.cuh"
 
 namespace sd {

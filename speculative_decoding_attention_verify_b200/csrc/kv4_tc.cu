@@ -33,11 +33,14 @@
 // lost to instruction fetch and a tile took 7,000 cycles).
 // K and V tiles, S and P are double-buffered: S of tile t overwrites the buffer of tile t - 2
 // once that tile's P V has completed.
-// Bound by the chain of those steps: with two buffers (TMEM has no room for a third beside O and Q)
-// a tile's S, its softmax and its P V follow one another, about 2,600 cycles a tile for 63 rows and
-// 128 channels, of which the softmax has 2,200; the tensor core is busy for 29% of the kernel's
-// time, issue slots for 42%, shared memory for 38%.  28 sequences of 26,033 positions, 4 KV heads,
-// 63 rows: 261 us, 1.5 TB/s.  Measured on the way, with codes not yet centred (then 250 us): every
+// Bound by the chain of those steps: with two buffers a tile's S, its softmax and its P V follow one
+// another, about 3,300 cycles a tile for 63 rows and 128 channels (154 tiles per CTA), of which the
+// softmax has 2,200; the tensor core is busy for 29% of the kernel's time, issue slots for 42%, shared
+// memory for 38%.  (A third buffer beside O needs Q in shared memory, where attn_tc.cu has it, and
+// with it a shorter ring; not built.)  28 sequences of 26,033 positions, 4 KV heads, 63 rows: 259 us,
+// 1.5 TB/s: no faster than attn_tc.cu over a bf16 cache, 252-260 us, which reads 3.8 times the bytes.
+// 70 rows 355 us and 126 rows 372 (one copy: a warp has all 128 columns).
+// Measured on the way, with codes not yet centred (then 250 us): every
 // expanding warp with its own cp.async ring instead of a copying warp 269; the positions' factors
 // loaded where they are used 274; 64 columns at a time 293.  Centred: one code for K's and V's
 // expansion 274, the four steps of an expansion unrolled together 275.

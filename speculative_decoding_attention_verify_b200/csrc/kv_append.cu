@@ -26,10 +26,16 @@
 // at fp32 cost.
 //
 // Measured (28 query and 4 KV heads of 128, bf16): 8 ragged prompts of up to 4,096 rows into pages
-// 77 us, 5.1 TB/s, bound by HBM; a prompt of 26,024 rows into a 4-bit cache 124 us, 4.0 TB/s, bound
-// by issue slots (fp64 rotations of the keys, minima and maxima, codes).  (With the chunks in a
-// structure that the compiler kept in local memory: 115 and 170.)  A decode step's row 6.2 us (4
-// bits: 8.0), of which the kernel has 3.5 (5.2): launch and the loads that depend on one another.
+// 81 us, 4.8 TB/s; a prompt of 26,024 rows into a 4-bit cache 127 us, 3.9 TB/s.  Neither is at a
+// limit of the chip: HBM is busy for 55 and 46%, issue slots for 64 and 66%, the ALU pipe for 47 and
+// 43%, fp64 for 4% (4 bits).  Warps wait for global loads (2.4 and 2.2 of 10 per issue): a block
+// looks up, forms its cosines and meets a barrier before it turns anything, and the 4-bit keys' and
+// values' loads come after the queries'.  At 64 registers (4 blocks per SM) the bf16 kernels spill
+// 36 bytes, with 4-bit caches 160, which is 4% of the instructions.  (With the chunks in a structure
+// that the compiler kept in local memory as a whole: 115 and 170 us.)  13,012 fp32 rows: 80 us (0.91
+// of the copy rate), into 4 bits 88.  append_narrow_kernel: the prompt of 26,024 bf16 rows with a
+// rotated part of 24 channels 175 us, into 4 bits 333.  A decode step's row 6.2 us (4 bits: 8.1), of
+// which the kernel has 3.5 (5.2): launch and the loads that depend on one another.
 #include <math.h>
 
 #include <cuda_bf16.h>

@@ -21,9 +21,9 @@ namespace sd {
 // hint) when it has no work.
 __device__ __forceinline__ bool kv4_sequence(const Kv4Params &p, int b, int &q0, int &n_q,
                                              int &kv_len, bool &bad) {
-    q0 = __ldg(p.q_start + b);
-    n_q = __ldg(p.q_start + b + 1) - q0;
-    kv_len = __ldg(p.kv_len + b);
+    q0 = ld_dep(p.q_start + b);
+    n_q = ld_dep(p.q_start + b + 1) - q0;
+    kv_len = ld_dep(p.kv_len + b);
     bad = false;
     if (n_q == 0) return false;
     bad = n_q < 0 || n_q > p.max_q_rows || q0 < 0 || q0 + n_q > p.rows_cap || kv_len < n_q ||
@@ -35,7 +35,7 @@ __device__ __forceinline__ bool kv4_sequence(const Kv4Params &p, int b, int &q0,
 __device__ __forceinline__ int64_t kv4_row(const Kv4Params &p, int b, int h, int j) {
     if (p.page_size == 0)
         return (int64_t)b * p.stride_b + (int64_t)h * p.stride_h + j;
-    const int page = __ldg(p.block_table + (int64_t)b * p.max_pages + (j >> 4));
+    const int page = ld_dep(p.block_table + (int64_t)b * p.max_pages + (j >> 4));
     if (page < 0 || page >= p.num_pages) {
         set_dev_err(p.dev_err, SD_DEVERR_PAGE);
         return -1;
@@ -163,9 +163,9 @@ struct Kv4Cursor {
         tiles = 1;
         kv_len = 0;
         if (b >= p.batch) return;
-        q0 = __ldg(p.q_start + b);
-        n_q = __ldg(p.q_start + b + 1) - q0;
-        kv_len = __ldg(p.kv_len + b);
+        q0 = ld_dep(p.q_start + b);
+        n_q = ld_dep(p.q_start + b + 1) - q0;
+        kv_len = ld_dep(p.kv_len + b);
         tiles = (kv_len + p.tile - 1) / p.tile;
     }
     // n tiles on, within the unit or to the start of the next one.

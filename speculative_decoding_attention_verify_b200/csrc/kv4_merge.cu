@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const Kv4Params p) 
     int64_t first, step;  // slots first, first + step, ... (tensor cores: after the first one)
     int n;
     if (p.ctas) {
-        const int2 c = __ldg(kv4_unit_ctas(p) + u);
+        const int2 c = ld_dep(kv4_unit_ctas(p) + u);
         n = c.y - c.x + 1;
         if (n == 1) return;  // the output is there already
         first = 2 * (int64_t)c.x;

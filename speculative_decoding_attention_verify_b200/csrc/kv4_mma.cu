@@ -157,7 +157,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
         for (int i = 0; i < 2; ++i) {
             const int j = pc.t * kTile + warp * kPos + i * kPageSize;
             pages[i] = p.page_size && j < pc.kv_len
-                           ? __ldg(p.block_table + (int64_t)pc.b * p.max_pages + (j >> 4))
+                           ? ld_dep(p.block_table + (int64_t)pc.b * p.max_pages + (j >> 4))
                            : 0;
         }
     };
@@ -240,7 +240,7 @@ kv4_mma_kernel(const __grid_constant__ Kv4Params p) {
             float sum = 0.f, top = 0.f;
 #pragma unroll
             for (int w = 0; w < kW; ++w) {
-                x[w] = has ? __ldg(src + w) : make_uint4(0u, 0u, 0u, 0u);
+                x[w] = has ? ld_dep(src + w) : make_uint4(0u, 0u, 0u, 0u);
                 float f[8];
                 Chunk<true>::to_float(x[w], f);
 #pragma unroll

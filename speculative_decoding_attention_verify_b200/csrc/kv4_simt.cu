@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(kThreads) kv4_simt_kernel(const Kv4Params p, i
                 uint2 q = make_uint2(0u, 0u);
                 uint32_t par = 0u;
                 if (row >= 0) {
-                    q = __ldg(reinterpret_cast<const uint2 *>((w ? p.v : p.k) + row * (D / 2)) + c);
-                    par = __ldg((w ? p.vp : p.kp) + row);
+                    q = ld_dep(reinterpret_cast<const uint2 *>((w ? p.v : p.k) + row * (D / 2)) + c);
+                    par = ld_dep((w ? p.vp : p.kp) + row);
                 }
                 const float sc = param_scale(par), lo = param_low(par);
 #pragma unroll

@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
         auto look_up = [&]() {  // this lane's page of the next tile
             const int j = pc.t * kTile + (lane & 7) * kPageSize;
             return p.page_size && j < pc.kv_len
-                       ? __ldg(p.block_table + (int64_t)pc.b * p.max_pages + (j >> 4))
+                       ? ld_dep(p.block_table + (int64_t)pc.b * p.max_pages + (j >> 4))
                        : 0;
         };
         int page = look_up();
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const __grid_consta
             const uint4 *src = reinterpret_cast<const uint4 *>(
                 static_cast<const unsigned short *>(p.q) +
                 ((int64_t)(u.q0 + (has ? r / G : 0)) * p.h_q + u.g * G + (has ? r % G : 0)) * D);
-            auto load = [&](int c) { return has ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u); };
+            auto load = [&](int c) { return has ? ld_dep(src + c) : make_uint4(0u, 0u, 0u, 0u); };
             uint32_t top = 0;  // largest magnitudes of both halves, as bits
             float2 sum = make_float2(0.f, 0.f);
             uint4 x[D / 8];

@@ -59,7 +59,7 @@ __device__ __forceinline__ int find_sequence(const int32_t *q_start, int batch, 
     int lo = 0, n = batch;
     while (n > 0) {
         const int step = (n + 31) / 32, idx = lo + step * (lane + 1);
-        const bool le = idx <= lo + n && __ldg(q_start + idx) <= r;
+        const bool le = idx <= lo + n && ld_dep(q_start + idx) <= r;
         const int cnt = __popc(__ballot_sync(0xffffffffu, le));
         const int hi = lo + n;
         lo += step * cnt;
@@ -144,8 +144,8 @@ __device__ __forceinline__ RowInfo find_row(const AppendParams &p, int r, int la
     RowInfo f{0, 0, 0, 0};
     const int b = find_sequence(p.q_start, p.batch, r, lane);
     if (b >= p.batch) return f;
-    const int q0 = __ldg(p.q_start + b), q1 = __ldg(p.q_start + b + 1), n = q1 - q0;
-    const int len = __ldg(p.kv_len + b);
+    const int q0 = ld_dep(p.q_start + b), q1 = ld_dep(p.q_start + b + 1), n = q1 - q0;
+    const int len = ld_dep(p.kv_len + b);
     if (q0 < 0 || q0 > r || r >= q1) return f;
     if (q1 > p.n_rows || len < n || len > p.max_kv_len ||
         (p.page_size && len > (int64_t)p.max_pages * kPageSize)) {
@@ -156,7 +156,7 @@ __device__ __forceinline__ RowInfo find_row(const AppendParams &p, int r, int la
     f.j = len - n + (r - q0);
     f.flags = 3;
     if (p.page_size) {
-        f.page = __ldg(p.block_table + (int64_t)b * p.max_pages + (f.j >> 4));
+        f.page = ld_dep(p.block_table + (int64_t)b * p.max_pages + (f.j >> 4));
         if (f.page < 0 || f.page >= p.num_pages) {
             if (lane == 0) set_dev_err(p.dev_err, SD_DEVERR_PAGE);
             f.flags = 1;
@@ -170,14 +170,14 @@ __device__ __forceinline__ RowInfo find_row(const AppendParams &p, int r, int la
 __device__ __forceinline__ void check_starts(const AppendParams &p) {
     if (blockIdx.x != 0) return;
     for (int b = threadIdx.x; b < p.batch; b += kThreads) {
-        const int q0 = __ldg(p.q_start + b), q1 = __ldg(p.q_start + b + 1);
+        const int q0 = ld_dep(p.q_start + b), q1 = ld_dep(p.q_start + b + 1);
         if (q0 < 0 || q1 < q0 || q1 > p.n_rows) set_dev_err(p.dev_err, SD_DEVERR_SHAPE);
     }
 }
 
 // Position of row r, in turns of pair m, reduced to [-1/2, 1/2].
 __device__ __forceinline__ double turn_of(const AppendParams &p, const RowInfo &f, int r, int m) {
-    const int pos = p.pos ? __ldg(p.pos + r) : f.j;
+    const int pos = p.pos ? ld_dep(p.pos + r) : f.j;
     const double t = (double)pos * p.rope.turns[m];
     return t - rint(t);
 }

@@ -43,6 +43,14 @@ __device__ __forceinline__ void pdl_trigger() {
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A load of what an earlier kernel of the stream may write while this one is resident already, as the
+// above allows: a plain load, which pdl_wait orders.  (__ldg may only read what nothing writes from the
+// kernel's start on.)
+template <typename T>
+__device__ __forceinline__ T ld_dep(const T *p) {
+    return *p;
+}
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t s, Args... args) {

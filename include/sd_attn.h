@@ -597,7 +597,7 @@ SD_API sd_status sd_kv4_attention_workspace_size(const sd_q_desc *q, const sd_kv
  * below a step's largest term.  Over 140,000 random positions all this is off by 2e-4 of the output
  * (rms), beside its own rounding.
  * A row of V of one value (s = 0) counts with s = 2^-8 |lo| there, and one whose s is then below
- * 2^-90 with s = 2^-90; a position whose weight times s is below 2^-136 of its row's largest does
+ * 2^-90 with s = 2^-90; a position whose weight times s is below 2^-136 of its row's largest need
  * not count at all.  s is neither negative nor NaN (what sd_kv4_append writes).
  * bf16 rows run on tensor cores (up to 128 rows per KV head, q_data and out 16-byte aligned), the
  * rest, without that rounding and those bounds, on CUDA cores, many times slower.  The kernel for 17
